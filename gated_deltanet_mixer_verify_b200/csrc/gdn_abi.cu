@@ -634,6 +634,318 @@ gdn_status gdn_accept(const gdn_accept_shape* shape, const void* target_logits, 
     return launched(gdn::launch_accept(a, workspace, static_cast<cudaStream_t>(stream)), who);
 }
 
+// ---------------------------------------------------------------- paged attention layers
+
+// Checks shared by the three calls; max_T: the largest T the call takes.
+static gdn_status check_kv(const gdn_kv_shape* s, int max_T, const char* who) {
+    if (!s) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", who);
+    if (s->B < 0 || s->T < 1 || s->page_size < 1 || s->num_pages < 1)
+        return fail(GDN_ERR_INVALID_ARG, "%s: sizes must be positive (B may be 0)", who);
+    if (s->B > 65535) return fail(GDN_ERR_UNSUPPORTED, "%s: B %d > 65535", who, s->B);
+    if (s->T > max_T) return fail(GDN_ERR_UNSUPPORTED, "%s: T %d > %d", who, s->T, max_T);
+    if (s->page_size > 65536) return fail(GDN_ERR_UNSUPPORTED, "%s: page_size %d > 65536", who, s->page_size);
+    if (s->status_word && (reinterpret_cast<uintptr_t>(s->status_word) & 3u) != 0)
+        return fail(GDN_ERR_INVALID_ARG, "%s: status_word misaligned", who);
+    return GDN_OK;
+}
+
+static gdn_status check_table(const gdn_kv_shape* s, const char* who) {
+    if (s->max_pages < 1) return fail(GDN_ERR_INVALID_ARG, "%s: max_pages must be positive", who);
+    if ((int64_t)s->max_pages * s->page_size > (1 << 30))
+        return fail(GDN_ERR_UNSUPPORTED, "%s: max_pages * page_size > 2^30", who);
+    return GDN_OK;
+}
+
+static gdn_status check_heads(const gdn_kv_shape* s, const char* who) {
+    if (s->H_q < 1 || s->H_kv < 1 || s->d < 1)
+        return fail(GDN_ERR_INVALID_ARG, "%s: sizes must be positive (B may be 0)", who);
+    if (s->H_q % s->H_kv != 0)
+        return fail(GDN_ERR_INVALID_ARG, "%s: H_q (%d) is not a multiple of H_kv (%d)", who, s->H_q, s->H_kv);
+    if (s->dtype != GDN_F32 && s->dtype != GDN_BF16)
+        return fail(GDN_ERR_INVALID_ARG, "%s: dtype %d unknown", who, s->dtype);
+    if (s->H_q > 65535) return fail(GDN_ERR_UNSUPPORTED, "%s: H_q %d > 65535", who, s->H_q);
+    if (s->d != 64 && s->d != 128 && s->d != 256)
+        return fail(GDN_ERR_UNSUPPORTED, "%s: d %d not built (64, 128, 256)", who, s->d);
+    return GDN_OK;
+}
+
+static int64_t element_bytes(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
+
+// The cache's strides: 16-byte multiples, no two entries of an axis within one head's d elements.
+// (An axis with one entry may have any stride: it is never used.)
+static gdn_status check_cache(const gdn_kv_shape* s, const char* who) {
+    const int64_t es = element_bytes(s->dtype);
+    const struct { const char* name; int64_t stride; int64_t n; } ax[3] = {
+        {"page_stride", s->page_stride, s->num_pages},
+        {"slot_stride", s->slot_stride, s->page_size},
+        {"head_stride", s->head_stride, s->H_kv}};
+    for (const auto& a : ax) {
+        if (a.n == 1) continue;
+        if (a.stride < s->d || (a.stride * es) % 16 != 0)
+            return fail(GDN_ERR_INVALID_ARG, "%s: %s %lld must be at least d and a multiple of 16 bytes", who, a.name,
+                        (long long)a.stride);
+        if (a.stride > ((int64_t)1 << 40)) return fail(GDN_ERR_UNSUPPORTED, "%s: %s > 2^40", who, a.name);
+    }
+    return GDN_OK;
+}
+
+static gdn::PagedCache paged_cache(const gdn_kv_shape* s, const void* k, const void* v) {
+    gdn::PagedCache c;
+    c.k = const_cast<void*>(k);
+    c.v = const_cast<void*>(v);
+    c.page_stride = s->num_pages == 1 ? 0 : s->page_stride;
+    c.slot_stride = s->page_size == 1 ? 0 : s->slot_stride;
+    c.head_stride = s->H_kv == 1 ? 0 : s->head_stride;
+    c.page = s->page_size;
+    c.num_pages = s->num_pages;
+    return c;
+}
+
+gdn_status gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* seq_len_in, int32_t* seq_len_out,
+                       const int32_t* commit_len, const int32_t* block_len, const int32_t* add_len, const int32_t* n_pages_in,
+                       int32_t* n_pages_out, int32_t* block_table, int32_t* free_list, const int32_t* free_count_in,
+                       int32_t* free_count_out, int32_t* kv_len, int32_t* q_len, int64_t* slot_map, void* stream) {
+    const char* who = "gdn_kv_plan";
+    gdn_status st = check_kv(shape, 1 << 20, who);
+    if (st == GDN_OK) st = check_table(shape, who);
+    if (st != GDN_OK) return st;
+    REQUIRE_PTR(free_count_in, who);
+    REQUIRE_PTR(free_count_out, who);
+    if (shape->B > 0) {
+        REQUIRE_PTR(seq_len_in, who);
+        REQUIRE_PTR(seq_len_out, who);
+        if (commit_len) REQUIRE_PTR(commit_len, who);
+        if (block_len) REQUIRE_PTR(block_len, who);
+        if (add_len) REQUIRE_PTR(add_len, who);
+        REQUIRE_PTR(n_pages_in, who);
+        REQUIRE_PTR(n_pages_out, who);
+        REQUIRE_PTR(block_table, who);
+        REQUIRE_PTR(free_list, who);
+        REQUIRE_PTR(kv_len, who);
+        REQUIRE_PTR(q_len, who);
+        REQUIRE_PTR(slot_map, who);
+        // What the call writes may not be anything else that it reads or writes; a count's output
+        // may be its own input.
+        const size_t nb = (size_t)shape->B * 4;
+        const struct { const void* p; size_t n; int in; } out[] = {
+            {seq_len_out, nb, 0}, {n_pages_out, nb, 1}, {free_count_out, 4, 2}, {kv_len, nb, -1}, {q_len, nb, 5},
+            {slot_map, 2 * nb * shape->T, -1}, {block_table, nb * shape->max_pages, -1},
+            {free_list, (size_t)shape->num_pages * 4, -1}};
+        const struct { const void* p; size_t n; } in[] = {
+            {seq_len_in, nb}, {n_pages_in, nb}, {free_count_in, 4}, {commit_len, nb}, {add_len, nb}, {block_len, nb}};
+        const auto meet = [](const void* x, size_t n, const void* y, size_t m) {
+            const char* a = static_cast<const char*>(x);
+            const char* b = static_cast<const char*>(y);
+            return a < b + m && b < a + n;
+        };
+        for (int i = 0; i < 8; ++i) {
+            for (int j = 0; j < 6; ++j)
+                if (in[j].p && !(out[i].in == j && out[i].p == in[j].p) && meet(out[i].p, out[i].n, in[j].p, in[j].n))
+                    return fail(GDN_ERR_INVALID_ARG, "%s: an output overlaps an input", who);
+            for (int j = 0; j < i; ++j)
+                if (meet(out[i].p, out[i].n, out[j].p, out[j].n))
+                    return fail(GDN_ERR_INVALID_ARG, "%s: two outputs overlap", who);
+        }
+    }
+    gdn::KvPlanArgs a = {};
+    a.B = shape->B;
+    a.T = shape->T;
+    a.page = shape->page_size;
+    a.num_pages = shape->num_pages;
+    a.max_pages = shape->max_pages;
+    a.seq_in = seq_len_in;
+    a.seq_out = seq_len_out;
+    a.commit = commit_len;
+    a.block = block_len;
+    a.add = add_len;
+    a.held_in = n_pages_in;
+    a.held_out = n_pages_out;
+    a.table = block_table;
+    a.free_list = free_list;
+    a.count_in = free_count_in;
+    a.count_out = free_count_out;
+    a.kv_len = kv_len;
+    a.q_len = q_len;
+    a.slots = slot_map;
+    a.status_word = shape->status_word;
+    return launched(gdn::launch_kv_plan(a, static_cast<cudaStream_t>(stream)), who);
+}
+
+gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, const void* q, const void* k,
+                           const void* v, const float* inv_freq, const int32_t* positions, const int32_t* kv_len,
+                           const int32_t* q_len, const int64_t* slot_map, const float* q_norm, const float* k_norm,
+                           void* q_out, void* k_cache, void* v_cache, void* stream) {
+    const char* who = "gdn_rope_append";
+    gdn_status st = check_kv(shape, 1 << 20, who);
+    if (st == GDN_OK) st = check_heads(shape, who);
+    if (st == GDN_OK) st = check_cache(shape, who);
+    if (st != GDN_OK) return st;
+    if (!rope) return fail(GDN_ERR_INVALID_ARG, "%s: rope is NULL", who);
+    if (rope->rot < 16 || rope->rot % 16 != 0 || rope->rot > shape->d)
+        return fail(GDN_ERR_INVALID_ARG, "%s: rot %d must be a multiple of 16, 16..d", who, rope->rot);
+    if (rope->n_axes < 1 || rope->n_axes > 4)
+        return fail(GDN_ERR_INVALID_ARG, "%s: n_axes %d not in 1..4", who, rope->n_axes);
+    const int half = rope->rot / 2;
+    int64_t pairs = 0;
+    for (int i = 0; i < rope->n_axes; ++i) {
+        if (rope->sections[i] < 0) return fail(GDN_ERR_INVALID_ARG, "%s: a section is negative", who);
+        pairs += rope->sections[i];
+    }
+    if (pairs != half) return fail(GDN_ERR_INVALID_ARG, "%s: the sections must hold rot / 2 = %d pairs", who, half);
+    if ((rope->axes_interleaved | rope->pairs_interleaved) & ~1)
+        return fail(GDN_ERR_INVALID_ARG, "%s: axes_interleaved and pairs_interleaved must be 0 or 1", who);
+    if (rope->axes_interleaved)
+        for (int i = 1; i < rope->n_axes; ++i)
+            if (rope->sections[i] > 0 && i + (int64_t)rope->n_axes * (rope->sections[i] - 1) >= half)
+                return fail(GDN_ERR_INVALID_ARG, "%s: section %d does not fit in turn", who, i);
+    if (!(rope->norm_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "%s: norm_eps must be >= 0", who);
+    const int64_t es = element_bytes(shape->dtype);
+    const int64_t qw = (int64_t)shape->H_q * shape->d, kw = (int64_t)shape->H_kv * shape->d;
+    const int64_t tokens = (int64_t)shape->B * shape->T;
+    const struct { const char* name; int64_t stride, width; } ax[4] = {
+        {"q_stride", rope->q_stride, qw}, {"k_stride", rope->k_stride, kw},
+        {"v_stride", rope->v_stride, kw}, {"q_out_stride", rope->q_out_stride, qw}};
+    for (const auto& a : ax) {
+        if (a.stride < a.width || (a.stride * es) % 16 != 0)
+            return fail(GDN_ERR_INVALID_ARG, "%s: %s %lld must be at least a token's heads and a multiple of 16 bytes",
+                        who, a.name, (long long)a.stride);
+        if (a.stride > ((int64_t)1 << 32)) return fail(GDN_ERR_UNSUPPORTED, "%s: %s > 2^32", who, a.name);
+    }
+    if (tokens > ((int64_t)1 << 30)) return fail(GDN_ERR_UNSUPPORTED, "%s: B * T > 2^30", who);
+    if (shape->B == 0) return ok();
+    REQUIRE_PTR(q, who);
+    REQUIRE_PTR(k, who);
+    REQUIRE_PTR(v, who);
+    REQUIRE_PTR(inv_freq, who);
+    if (positions) {
+        REQUIRE_PTR(positions, who);
+    } else {
+        REQUIRE_PTR(kv_len, who);
+        REQUIRE_PTR(q_len, who);
+    }
+    REQUIRE_PTR(slot_map, who);
+    if (q_norm) REQUIRE_PTR(q_norm, who);
+    if (k_norm) REQUIRE_PTR(k_norm, who);
+    REQUIRE_PTR(q_out, who);
+    REQUIRE_PTR(k_cache, who);
+    REQUIRE_PTR(v_cache, who);
+    if (q_out == q) {
+        if (rope->q_out_stride != rope->q_stride)
+            return fail(GDN_ERR_INVALID_ARG, "%s: q_out in place needs q's stride", who);
+    } else {
+        const char* o = static_cast<const char*>(q_out);
+        const char* oe = o + ((tokens - 1) * rope->q_out_stride + qw) * es;
+        const void* ins[3] = {q, k, v};
+        for (int i = 0; i < 3; ++i) {
+            const char* x = static_cast<const char*>(ins[i]);
+            const char* xe = x + ((tokens - 1) * ax[i].stride + ax[i].width) * es;
+            if (o < xe && x < oe) return fail(GDN_ERR_INVALID_ARG, "%s: q_out overlaps an input", who);
+        }
+    }
+    gdn::RopeArgs a = {};
+    a.B = shape->B;
+    a.T = shape->T;
+    a.Hq = shape->H_q;
+    a.Hk = shape->H_kv;
+    a.d = shape->d;
+    a.bf16 = shape->dtype == GDN_BF16;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.q_stride = rope->q_stride;
+    a.k_stride = rope->k_stride;
+    a.v_stride = rope->v_stride;
+    a.qo_stride = rope->q_out_stride;
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    a.kv_len = kv_len;
+    a.q_len = q_len;
+    a.slots = slot_map;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = rope->norm_eps;
+    a.rot = rope->rot;
+    a.axes = rope->n_axes;
+    for (int i = 0; i < rope->n_axes; ++i) a.sections[i] = rope->sections[i];
+    a.axes_interleaved = rope->axes_interleaved != 0;
+    a.pairs_interleaved = rope->pairs_interleaved != 0;
+    a.cache = paged_cache(shape, k_cache, v_cache);
+    a.status_word = shape->status_word;
+    return launched(gdn::launch_rope_append(a, static_cast<cudaStream_t>(stream)), who);
+}
+
+static gdn_status check_attention(const gdn_kv_shape* s, const char* who) {
+    if (!s) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", who);
+    if (s->B < 0 || s->T < 1) return fail(GDN_ERR_INVALID_ARG, "%s: sizes must be positive (B may be 0)", who);
+    if (s->B > 65535) return fail(GDN_ERR_UNSUPPORTED, "%s: B %d > 65535", who, s->B);
+    if (s->T > 16) return fail(GDN_ERR_UNSUPPORTED, "%s: T %d > 16", who, s->T);
+    return check_heads(s, who);
+}
+
+size_t gdn_paged_attention_workspace_bytes(const gdn_kv_shape* shape) {
+    if (check_attention(shape, "gdn_paged_attention_workspace_bytes") != GDN_OK) return 0;
+    return gdn::paged_attention_workspace_bytes(shape->B, shape->T, shape->H_q, shape->H_kv, shape->d,
+                                                shape->dtype == GDN_BF16);
+}
+
+gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                               const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    const char* who = "gdn_paged_attention";
+    gdn_status st = check_attention(shape, who);
+    if (st == GDN_OK) st = check_kv(shape, 16, who);
+    if (st == GDN_OK) st = check_table(shape, who);
+    if (st == GDN_OK) st = check_cache(shape, who);
+    if (st != GDN_OK) return st;
+    if (shape->out_dtype != GDN_F32 && shape->out_dtype != GDN_BF16)
+        return fail(GDN_ERR_INVALID_ARG, "%s: out_dtype %d unknown", who, shape->out_dtype);
+    if (!(scale - scale == 0.f)) return fail(GDN_ERR_INVALID_ARG, "%s: scale must be a finite number", who);
+    if (window < 0) return fail(GDN_ERR_INVALID_ARG, "%s: window must be >= 0", who);
+    if (shape->B == 0) return ok();
+    REQUIRE_PTR(q, who);
+    REQUIRE_PTR(k_cache, who);
+    REQUIRE_PTR(v_cache, who);
+    REQUIRE_PTR(block_table, who);
+    REQUIRE_PTR(kv_len, who);
+    if (q_len) REQUIRE_PTR(q_len, who);
+    REQUIRE_PTR(o, who);
+    if (lse) REQUIRE_PTR(lse, who);
+    const size_t rows = (size_t)shape->B * shape->T * shape->H_q;
+    const char* qp = static_cast<const char*>(q);
+    const char* op = static_cast<const char*>(o);
+    if (qp < op + rows * shape->d * element_bytes(shape->out_dtype) && op < qp + rows * shape->d * element_bytes(shape->dtype))
+        return fail(GDN_ERR_INVALID_ARG, "%s: o overlaps q", who);
+    const size_t need = gdn::paged_attention_workspace_bytes(shape->B, shape->T, shape->H_q, shape->H_kv, shape->d,
+                                                             shape->dtype == GDN_BF16);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
+    if (workspace && !aligned16(workspace))
+        return fail(GDN_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", who);
+    gdn::AttnArgs a = {};
+    a.B = shape->B;
+    a.T = shape->T;
+    a.Hq = shape->H_q;
+    a.Hk = shape->H_kv;
+    a.d = shape->d;
+    a.max_pages = shape->max_pages;
+    a.window = window;
+    a.bf16 = shape->dtype == GDN_BF16;
+    a.out_bf16 = shape->out_dtype == GDN_BF16;
+    a.scale = scale;
+    a.q = q;
+    a.cache = paged_cache(shape, k_cache, v_cache);
+    a.table = block_table;
+    a.kv_len = kv_len;
+    a.q_len = q_len;
+    a.o = o;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status_word = shape->status_word;
+    return launched(gdn::launch_paged_attention(a, static_cast<cudaStream_t>(stream)), who);
+}
+
 gdn_status gdn_selftest_bounded_wait(int32_t* status_word, uint32_t polls, void* stream) {
     const char* who = "gdn_selftest_bounded_wait";
     if (!status_word || (reinterpret_cast<uintptr_t>(status_word) & 3u) != 0)

@@ -15,6 +15,9 @@ constexpr unsigned kFull = 0xffffffffu;
 // Status bits OR-ed into the caller's status word (see include/gdn.h).
 constexpr int kStatusBadAccept = 1;
 constexpr int kStatusWaitTimeout = 2;
+constexpr int kStatusBadLength = 4;
+constexpr int kStatusBadPage = 8;
+constexpr int kStatusNoPages = 16;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -169,6 +169,78 @@ cudaError_t launch_accept(AcceptArgs a, void* workspace, cudaStream_t stream);
 cudaError_t launch_accept_wait_selftest(int32_t* status_word, int32_t* next_token, uint32_t polls,
                                         cudaStream_t stream);
 
+// Block tables and slot maps (gdn_kv_plan.cu).
+struct KvPlanArgs {
+    int B, T, page, num_pages, max_pages;
+    const int32_t* seq_in;
+    int32_t* seq_out;
+    const int32_t* commit;       // or nullptr (0)
+    const int32_t* block;        // rows of the last block, or nullptr (no limit to the commit)
+    const int32_t* add;          // or nullptr (T)
+    const int32_t* held_in;
+    int32_t* held_out;
+    int32_t* table;              // [B][max_pages]
+    int32_t* free_list;          // [num_pages]
+    const int32_t* count_in;
+    int32_t* count_out;
+    int32_t* kv_len;
+    int32_t* q_len;
+    int64_t* slots;              // [B][T]
+    int32_t* status_word;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream);
+
+// A paged key / value cache: element (page, slot, head, j) at page * page_stride + slot *
+// slot_stride + head * head_stride + j, in elements.
+struct PagedCache {
+    void* k;
+    void* v;
+    int64_t page_stride, slot_stride, head_stride;
+    int page, num_pages;
+};
+
+// Rotary positions and the append to the cache (gdn_rope.cu).
+struct RopeArgs {
+    int B, T, Hq, Hk, d;
+    bool bf16;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    int64_t q_stride, k_stride, v_stride, qo_stride;   // elements between tokens
+    const float* inv_freq;
+    const int32_t* positions;    // [axes][B][T], or nullptr (kv_len - q_len + t)
+    const int32_t* kv_len;
+    const int32_t* q_len;
+    const int64_t* slots;
+    const float* q_norm;         // [d] or nullptr
+    const float* k_norm;
+    float eps;
+    int rot, axes, sections[4];
+    bool axes_interleaved, pairs_interleaved;
+    PagedCache cache;
+    int32_t* status_word;
+};
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t stream);
+
+// Attention over the paged cache (gdn_attn.cu).
+struct AttnArgs {
+    int B, T, Hq, Hk, d, max_pages, window;
+    bool bf16, out_bf16;
+    float scale;
+    const void* q;
+    PagedCache cache;
+    const int32_t* table;        // [B][max_pages]
+    const int32_t* kv_len;
+    const int32_t* q_len;        // or nullptr (T)
+    void* o;
+    float* lse;                  // or nullptr
+    void* workspace;
+    int32_t* status_word;
+};
+size_t paged_attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, bool bf16);
+cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);
+
 // One CTA per (sequence, value head) form for d_k = 128, d_v <= 128, T <= 16.
 bool head_kernel_applies(const VerifyArgs& a);
 

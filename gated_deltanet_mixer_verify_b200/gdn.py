@@ -21,6 +21,7 @@ _LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
 GDN_F32, GDN_BF16 = 0, 1
 STATUS_BAD_ACCEPT = 1
+STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_NO_PAGES = 4, 8, 16
 GDN_LAUNCH_PDL = 1   # gdn_shape.launch_flags: programmatic dependent launch (include/gdn.h)
 
 
@@ -44,6 +45,21 @@ class _AcceptShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("logits_dtype", ctypes.c_int32), ("sampled", ctypes.c_int32),
                 ("temperature", ctypes.c_float)]
+
+
+class _KvShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("status_word", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("axes_interleaved", ctypes.c_int32), ("pairs_interleaved", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -81,7 +97,13 @@ def _load():
     lib.gdn_verify_step_gated.argtypes = [S] + [_VP] * 12 + [ctypes.c_float] + [_VP] * 3
     lib.gdn_gated_rmsnorm.argtypes = [ctypes.c_int64, ctypes.c_int32, _VP, ctypes.c_int32, _VP, ctypes.c_int32,
                                       _VP, ctypes.c_float, _VP, ctypes.c_int32, _VP]
-    for fn in ("gdn_verify_step", "gdn_commit", "gdn_decode_step", "gdn_commit_and_verify", "gdn_chunk_prefill",
+    K = ctypes.POINTER(_KvShape)
+    lib.gdn_kv_plan.argtypes = [K] + [_VP] * 15
+    lib.gdn_rope_append.argtypes = [K, ctypes.POINTER(_Rope)] + [_VP] * 14
+    lib.gdn_paged_attention.argtypes = ([K, ctypes.c_float, ctypes.c_int32] + [_VP] * 9 + [ctypes.c_size_t, _VP])
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [K]
+    lib.gdn_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+    for fn in ("gdn_kv_plan", "gdn_rope_append", "gdn_paged_attention", "gdn_verify_step", "gdn_commit", "gdn_decode_step", "gdn_commit_and_verify", "gdn_chunk_prefill",
                "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_prepare", "gdn_chunk_prefill_scan",
                "gdn_short_conv", "gdn_verify_step_gated", "gdn_gated_rmsnorm", "gdn_accept",
                "gdn_selftest_bounded_wait", "gdn_selftest_accept_wait"):
@@ -471,3 +493,188 @@ def chunk_prefill_noalloc(q, k, v, a, b, A_log, dt_bias, state_in=None, state_ou
                                              *_ptrs(q, k, v, a, b, A_log, dt_bias, state_in, state_out, o),
                                              _stream(stream)))
     return o, state_out
+
+
+def _one_type(dt, **ts):
+    for name, t in ts.items():
+        if t is not None and t.dtype != dt:
+            raise TypeError("%s must be %s, not %s" % (name, str(dt)[6:], t.dtype))
+
+
+def _one_shape(shape, **ts):
+    for name, t in ts.items():
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError("%s must be %s, not %s" % (name, list(shape), list(t.shape)))
+
+
+def _strided_ptrs(*ts):
+    """Device pointers of tensors whose strides the call takes: on the current device, their last
+    axis contiguous (what the other strides may be is the caller's to check)."""
+    cur = torch.cuda.current_device() if ts[0].is_cuda else None
+    out = []
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if t.get_device() != cur:
+            raise ValueError("tensor is on cuda:%d but the current CUDA device is cuda:%d; call under "
+                             "torch.cuda.device(%d)" % (t.get_device(), cur, t.get_device()))
+        if t.stride(-1) != 1:
+            raise ValueError("expected a contiguous last axis")
+        out.append(t.data_ptr())
+    return out
+
+
+def _token_stride(name, t) -> int:
+    """Elements between the tokens of t [B, T, heads, d] (its heads contiguous within a token, its
+    sequences T tokens apart): a slice of a projection's output, or a contiguous tensor."""
+    B, T, H, d = t.shape
+    sb, st, sh, _ = t.stride()
+    if T == 1:
+        st = sb if B > 1 else H * d
+    if (H > 1 and sh != d) or (B > 1 and sb != T * st):
+        raise ValueError("%s must be [B, T, heads, d] with one stride from token to token and contiguous heads" % name)
+    return st
+
+
+def _kv_shape(B, T, H_q, H_kv, d, dtype, out_dtype, page_size, num_pages, max_pages, strides, status_word) -> _KvShape:
+    if status_word is not None:
+        _one_type(torch.int32, status_word=status_word)
+    return _KvShape(B, T, H_q, H_kv, d, dtype, out_dtype, page_size, num_pages, max_pages, *strides,
+                    _ptr(status_word))
+
+
+def _cache_strides(k_cache, v_cache, H_kv, d, dtype):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (H_kv, d):
+        raise ValueError("k_cache and v_cache must be [pages, page_size, %d, %d]" % (H_kv, d))
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("the caches must have the dtype of q (%s)" % dtype)
+    strides = k_cache.stride()
+    if strides != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return strides[:3]
+
+
+def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, commit_len=None, add_len=None,
+            block_len=None, seq_len_out=None, n_pages_out=None, free_count_out=None, kv_len=None, q_len=None, slot_map=None,
+            status_word=None, stream=None):
+    """Block tables and slot maps of the next block, on the GPU: ``commit_len`` [B] of the last
+    block's tokens are kept (``block_len`` [B], the last call's q_len: at most that many), ``add_len`` [B] new ones (None: T each; -1: the request has ended) get
+    their pages and slots. seq_len, n_pages [B], block_table [B, max_pages], free_list [pages] and
+    free_count [1] are int32 and updated in place unless the ``_out`` arrays are given. Returns
+    (kv_len [B] int32, q_len [B] int32, slot_map [B, T] int64)."""
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    seq_len_out = seq_len if seq_len_out is None else seq_len_out
+    n_pages_out = n_pages if n_pages_out is None else n_pages_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    if kv_len is None:
+        kv_len = torch.empty(B, dtype=torch.int32, device=dev)
+    if q_len is None:
+        q_len = torch.empty(B, dtype=torch.int32, device=dev)
+    if slot_map is None:
+        slot_map = torch.empty((B, T), dtype=torch.int64, device=dev)
+    per_seq = dict(seq_len=seq_len, seq_len_out=seq_len_out, n_pages=n_pages, n_pages_out=n_pages_out, commit_len=commit_len,
+                   add_len=add_len, block_len=block_len, kv_len=kv_len, q_len=q_len)
+    _one_type(torch.int32, block_table=block_table, free_list=free_list, free_count=free_count,
+              free_count_out=free_count_out, **per_seq)
+    _one_type(torch.int64, slot_map=slot_map)
+    _one_shape((B,), **per_seq)
+    _one_shape((1,), free_count=free_count, free_count_out=free_count_out)
+    _one_shape((B, T), slot_map=slot_map)
+    if free_list.dim() != 1:
+        raise ValueError("free_list must be [pages]")
+    sh = _kv_shape(B, T, 1, 1, 64, GDN_BF16, GDN_BF16, page_size, free_list.shape[0], max_pages, (0, 0, 0), status_word)
+    _check(_load().gdn_kv_plan(ctypes.byref(sh), *_ptrs(seq_len, seq_len_out, commit_len, block_len, add_len, n_pages, n_pages_out,
+                                                       block_table, free_list, free_count, free_count_out, kv_len,
+                                                       q_len, slot_map), _stream(stream)))
+    return kv_len, q_len, slot_map
+
+
+def rope_append(q, k, v, inv_freq, k_cache, v_cache, slot_map, positions=None, kv_len=None, q_len=None, sections=None,
+                axes_interleaved=False, pairs_interleaved=False, q_norm=None, k_norm=None, norm_eps=1e-6, q_out=None,
+                status_word=None, stream=None):
+    """Rotary positions and the append to the paged cache. q [B, T, H_q, d], k and v [B, T, H_kv, d]
+    (one stride from token to token, so slices of one projection's output will do) are normalised
+    head by head (``q_norm``, ``k_norm`` [d] fp32, or None), rotated by positions [axes, B, T] int32
+    (None: kv_len - q_len + t, both [B]) times inv_freq [rot / 2] fp32, and k, v go to ``slot_map``
+    [B, T] int64 (-1: none) of the caches [pages, page_size, H_kv, d]. ``sections``: rotated pairs of
+    each axis (None: one axis). Returns q_out (may be q)."""
+    B, T, H_q, d = q.shape
+    H_kv = k.shape[2]
+    if tuple(k.shape) != (B, T, H_kv, d) or v.shape != k.shape:
+        raise ValueError("q [B,T,H_q,d] and k, v [B,T,H_kv,d] disagree")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k, v must share a dtype")
+    strides = _cache_strides(k_cache, v_cache, H_kv, d, q.dtype)
+    rot = 2 * inv_freq.shape[0]
+    sections = [rot // 2] if sections is None else list(sections)
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("one to four sections")
+    if q_out is None:
+        q_out = torch.empty((B, T, H_q, d), dtype=q.dtype, device=q.device)
+    if q_out.dtype != q.dtype:
+        raise TypeError("q_out must have q's dtype")
+    _one_shape((B, T, H_q, d), q_out=q_out)
+    _one_type(torch.float32, inv_freq=inv_freq, q_norm=q_norm, k_norm=k_norm)
+    _one_shape((rot // 2,), inv_freq=inv_freq)
+    _one_shape((d,), q_norm=q_norm, k_norm=k_norm)
+    _one_type(torch.int64, slot_map=slot_map)
+    _one_shape((B, T), slot_map=slot_map)
+    if positions is not None:
+        _one_type(torch.int32, positions=positions)
+        _one_shape((len(sections), B, T), positions=positions)
+        kv_len = q_len = None
+    else:
+        _one_type(torch.int32, kv_len=kv_len, q_len=q_len)
+        _one_shape((B,), kv_len=kv_len, q_len=q_len)
+    dt = _dtype_code(q.dtype)
+    sh = _kv_shape(B, T, H_q, H_kv, d, dt, dt, k_cache.shape[1], k_cache.shape[0], 1, strides, status_word)
+    rp = _Rope(rot, len(sections), (ctypes.c_int32 * 4)(*sections), int(bool(axes_interleaved)), int(bool(pairs_interleaved)),
+               float(norm_eps), _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
+               _token_stride("q_out", q_out))
+    pq, pk, pv, po, pkc, pvc = _strided_ptrs(q, k, v, q_out, k_cache, v_cache)
+    _check(_load().gdn_rope_append(ctypes.byref(sh), ctypes.byref(rp), pq, pk, pv,
+                                   *_ptrs(inv_freq, positions, kv_len, q_len, slot_map, q_norm, k_norm), po, pkc, pvc,
+                                   _stream(stream)))
+    return q_out
+
+
+def paged_attention_workspace_bytes(B, T, H_q, H_kv, d, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace :func:`paged_attention` needs."""
+    dt = _dtype_code(dtype)
+    sh = _KvShape(B, T, H_q, H_kv, d, dt, dt, 1, 1, 1, 0, 0, 0, None)
+    return int(_load().gdn_paged_attention_workspace_bytes(ctypes.byref(sh)))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=None, window=0, o=None, lse=None,
+                    out_dtype=None, workspace=None, status_word=None, stream=None):
+    """Attention of q [B, T, H_q, d] (T = 1, or a verify block up to 16) over the paged caches
+    [pages, page_size, H_kv, d]: row t < q_len[b] (None: T) stands at kv_len[b] - q_len[b] + t of the
+    sequence whose pages block_table [B, max_pages] lists, and sees up to itself (``window`` > 0: that
+    many positions at most). ``scale`` defaults to d ** -0.5; ``lse`` [B, T, H_q] fp32 receives
+    the log of the softmax's sum. Returns o (``out_dtype``, default q's)."""
+    B, T, H_q, d = q.shape
+    H_kv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    strides = _cache_strides(k_cache, v_cache, H_kv, d, q.dtype)
+    if o is None:
+        o = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    elif out_dtype is not None and o.dtype != out_dtype:
+        raise TypeError("o is %s but out_dtype is %s" % (o.dtype, out_dtype))
+    _one_shape((B, T, H_q, d), o=o)
+    _one_type(torch.float32, lse=lse)
+    _one_shape((B, T, H_q), lse=lse)
+    _one_type(torch.int32, block_table=block_table, kv_len=kv_len, q_len=q_len)
+    _one_shape((B,), kv_len=kv_len, q_len=q_len)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    sh = _kv_shape(B, T, H_q, H_kv, d, _dtype_code(q.dtype), _dtype_code(o.dtype), k_cache.shape[1], k_cache.shape[0],
+                   block_table.shape[1], strides, status_word)
+    lib = _load()
+    if workspace is None:
+        need = lib.gdn_paged_attention_workspace_bytes(ctypes.byref(sh))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    kc, vc = _strided_ptrs(k_cache, v_cache)
+    pq, *rest = _ptrs(q, block_table, kv_len, q_len, o, lse, workspace)
+    _check(lib.gdn_paged_attention(ctypes.byref(sh), d ** -0.5 if scale is None else float(scale), int(window), pq, kc, vc,
+                                   *rest, _nbytes(workspace), _stream(stream)))
+    return o

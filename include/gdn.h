@@ -67,7 +67,9 @@
 extern "C" {
 #endif
 
-/* 10: gdn_selftest_accept_wait; 9: gdn_last_verify_kernel; 8: gdn_shape.launch_flags (GDN_LAUNCH_PDL); 7: prefill in pieces (gdn_chunk_prefill_pieces);
+/* Additions that change no struct and no call keep the number: a caller that needs gdn_kv_plan,
+ * gdn_rope_append or gdn_paged_attention looks the symbol up (they came after 10 was set).
+ * 10: gdn_selftest_accept_wait; 9: gdn_last_verify_kernel; 8: gdn_shape.launch_flags (GDN_LAUNCH_PDL); 7: prefill in pieces (gdn_chunk_prefill_pieces);
  * 6: gdn_accept; 5: gated norm; 4: gdn_short_conv; 3: commit-and-verify */
 #define GDN_ABI_VERSION 10
 
@@ -85,6 +87,11 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 #define GDN_STATUS_BAD_ACCEPT 1     /* an accept_len[b] was outside 0..T: nothing committed for b */
 #define GDN_STATUS_WAIT_TIMEOUT 2   /* a bounded wait for an asynchronous copy ran out: the
                                        affected heads were not written */
+#define GDN_STATUS_BAD_LENGTH 4     /* a length, row count or page count was out of its range:
+                                       see the call for what was left undone */
+#define GDN_STATUS_BAD_PAGE 8       /* a page id or slot outside the pool: masked, or not written */
+#define GDN_STATUS_NO_PAGES 16      /* the pool or a block table was too small: that sequence
+                                       got no new tokens */
 
 /*
  * Problem description shared by all calls. Sizes supported by this build:
@@ -394,6 +401,140 @@ gdn_status gdn_accept(const gdn_accept_shape* shape, const void* target_logits, 
 
 /* Bytes of workspace gdn_accept needs (0 for an invalid shape). */
 size_t gdn_accept_workspace_bytes(const gdn_accept_shape* shape);
+
+/*
+ * The attention layers beside the mixer (the 3 : 1 hybrid runs one after every three Gated
+ * DeltaNet layers; "Lithos-metal: Qwen3.8-27B on 40-core M5 Max", megakernel table, and "Qwen 3.8
+ * 27B mac m5: 200 tok/s, audited", DSpark section: the KV cache is rewound together with the
+ * recurrent state). One round of a verify loop is
+ *   gdn_kv_plan (commits the last block at its accept counts, hands out pages, builds the slots)
+ *   -> per attention layer: gdn_rope_append, gdn_paged_attention -> gdn_accept -> gdn_kv_plan ...
+ * and never leaves the GPU: every length below is read on the device.
+ *
+ * Paged cache: a pool of num_pages pages of page_size slots each. Element (page, slot, head, j)
+ * of k_cache is k_cache[page * page_stride + slot * slot_stride + head * head_stride + j], and
+ * v_cache has the same strides (in elements; each a multiple of 16 bytes, and at least d where
+ * its axis has more than one entry). So pages may be stored token by token or head by head, and
+ * keys and values may share one allocation. Position i of sequence b lives in page
+ * block_table[b][i / page_size], slot i % page_size. What a page holds behind a sequence's length
+ * is never used, whatever it is (infinities and NaN included).
+ */
+typedef struct {
+    int32_t B, T;            /* sequences; rows (new tokens) per sequence in this call */
+    int32_t H_q, H_kv, d;    /* query heads, key / value heads (H_q % H_kv == 0), head size */
+    int32_t dtype;           /* gdn_dtype of q, k, v and the caches */
+    int32_t out_dtype;       /* gdn_dtype of o (gdn_paged_attention) */
+    int32_t page_size;       /* slots per page: 1..65536 */
+    int32_t num_pages;       /* pages in the pool */
+    int32_t max_pages;       /* width of the block table; max_pages * page_size <= 2^30 */
+    int64_t page_stride, slot_stride, head_stride;
+    int32_t* status_word;    /* device int32 or NULL; bits GDN_STATUS_* are OR-ed in */
+} gdn_kv_shape;
+
+/*
+ * gdn_kv_plan -- block tables and slot maps from the requests' lengths, on the GPU, and the pool
+ * of pages behind them. Uses B (0..65535), T (1..2^20), page_size, num_pages, max_pages and
+ * status_word of the shape. For every sequence b, in one call:
+ *   len  = seq_len_in[b] + commit_len[b]         (NULL: + 0) the last block's accepted tokens stay,
+ *                                                the rest of it is forgotten
+ *          block_len (NULL: no limit) is the q_len of the last block: a commit above it counts as it,
+ *          so that gdn_accept's count (1 or more) commits nothing for a sequence that had no rows
+ *   add  = add_len[b]                            (NULL: T) new tokens, 0..T; -1: the request has
+ *                                                ended, its length becomes 0 and its pages return
+ *   want = ceil((len + add) / page_size) pages; fewer than it holds: the ones behind return to the
+ *          pool; more: new ones come from it
+ *   seq_len_out[b] = len, n_pages_out[b] = pages held now, kv_len[b] = len + add, q_len[b] = add,
+ *   slot_map[b][t] = slot of position len + t for t < add, -1 for the rest;
+ *   slot = page * page_size + offset.
+ * kv_len and q_len are what gdn_paged_attention takes, slot_map what gdn_rope_append takes.
+ *   block_table  [B][max_pages] in place; entries behind n_pages_out[b] are left as they were.
+ *   free_list    [num_pages] in place: a stack, its first free_count entries are the free pages.
+ *                All returned pages are pushed first, in order of b and of the pages within b; then
+ *                pages are popped from the top, in the same order. The result is deterministic.
+ *   *_in, *_out  may be the same array each (in place), and so may block_len and q_len.
+ *   kv_len, q_len [B] int32 out; slot_map [B][T] int64 out.
+ * A commit or block_len that is negative, or a commit that reaches behind the pages held, commits
+ * nothing for b (GDN_STATUS_BAD_ACCEPT) and the rest goes on. An add outside -1..T counts as 0, and a sequence
+ * whose seq_len_in or n_pages_in cannot be (negative, above max_pages, or a length behind the pages)
+ * keeps them with kv_len = q_len = 0 (both GDN_STATUS_BAD_LENGTH). Growth is granted in order of b
+ * until the first sequence that does not fit into what is free: it and every later one that needs
+ * pages get none, and neither does one that would need more than max_pages; their q_len is 0 and
+ * their kv_len is len (GDN_STATUS_NO_PAGES).
+ */
+gdn_status gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* seq_len_in, int32_t* seq_len_out,
+                       const int32_t* commit_len, const int32_t* block_len, const int32_t* add_len,
+                       const int32_t* n_pages_in, int32_t* n_pages_out, int32_t* block_table,
+                       int32_t* free_list, const int32_t* free_count_in, int32_t* free_count_out,
+                       int32_t* kv_len, int32_t* q_len, int64_t* slot_map, void* stream);
+
+/*
+ * gdn_rope_append -- rotary positions with one to four axes, and the append to the paged cache.
+ * For every token (b, t) whose slot is not negative:
+ *   q_out = R(N(q, q_norm)), k_cache[slot] = R(N(k, k_norm)), v_cache[slot] = v, where per head
+ *   N(x, w) = x / sqrt(mean(x^2) + norm_eps) * w          (w NULL: x)
+ *   R turns pair i < rot / 2 of the head's first rot elements by the angle p * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos); a, b are elements i and i + rot / 2, or 2 i and
+ *     2 i + 1 (pairs_interleaved); elements from rot on stay as they are;
+ *     p = positions[axis(i)][b][t]; positions NULL: kv_len[b] - q_len[b] + t on every axis
+ *   axis(i): axes_interleaved 0: the first sections[0] pairs belong to axis 0, the next
+ *     sections[1] to axis 1, ...; 1: axis a = i % n_axes while i < n_axes * sections[a], else 0.
+ * Angles are formed and reduced in fp64 (a far position times a frequency keeps nothing in fp32),
+ * everything else is fp32, and each result is rounded once to dtype. v is copied.
+ * A token with a negative slot writes nothing (its row of q_out stays as it was); one with a slot
+ * outside the pool writes nothing and sets GDN_STATUS_BAD_PAGE. The slots of one call must differ.
+ *   shape      B (0..65535), T (1..2^20), H_q, H_kv, d (64, 128 or 256), dtype, page_size, num_pages,
+ *              the strides and status_word; max_pages is not used.
+ *   q, q_out   [B][T] tokens q_stride (q_out_stride) elements apart, [H_q][d] contiguous within one;
+ *              k, v likewise (H_kv heads). So q, k, v may be slices of one projection's output.
+ *              q_out may be q (same stride), else it must not overlap q, k or v.
+ *   inv_freq   [rot / 2] fp32;  q_norm, k_norm [d] fp32 or NULL each.
+ *   positions  [n_axes][B][T] int32, or NULL (then kv_len and q_len [B] are required).
+ *   slot_map   [B][T] int64.
+ */
+typedef struct {
+    int32_t rot;                 /* rotated elements per head: a multiple of 16, up to d */
+    int32_t n_axes;              /* 1..4 */
+    int32_t sections[4];         /* pairs of each axis, rot / 2 in all */
+    int32_t axes_interleaved;    /* 0 or 1 */
+    int32_t pairs_interleaved;   /* 0 or 1 */
+    float norm_eps;              /* >= 0 */
+    int64_t q_stride, k_stride, v_stride, q_out_stride;   /* elements between tokens, 16-byte multiples */
+} gdn_rope;
+
+gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, const void* q, const void* k,
+                           const void* v, const float* inv_freq, const int32_t* positions,
+                           const int32_t* kv_len, const int32_t* q_len, const int64_t* slot_map,
+                           const float* q_norm, const float* k_norm, void* q_out, void* k_cache,
+                           void* v_cache, void* stream);
+
+/*
+ * gdn_paged_attention -- attention of one new token (T = 1) or of a verify block (T up to 16) over
+ * the paged cache, the block's own keys and values included (append first). Row (b, t), t < q_len[b],
+ * stands at position p = kv_len[b] - q_len[b] + t and sees positions max(0, p - window + 1) .. p
+ * (window 0: from 0). For query head h, with key head h / (H_q / H_kv):
+ *   s_j = scale q . k_j,   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}
+ * A row that sees nothing (p < 0) gives o = 0 and lse = -infinity. What a row does not see cannot
+ * change it, infinities and NaN included.
+ *   q        [B][T][H_q][d] dtype (contiguous), o the same in out_dtype, lse [B][T][H_q] fp32 or NULL.
+ *   block_table [B][max_pages] int32, kv_len [B] int32, q_len [B] int32 or NULL (T rows each).
+ *   Rows t >= q_len[b] are left as they were in o and lse. A sequence with kv_len[b] outside
+ *   0..max_pages * page_size or q_len[b] outside 0..T writes nothing (GDN_STATUS_BAD_LENGTH).
+ *   Positions on a page id outside the pool are not seen (GDN_STATUS_BAD_PAGE).
+ *   workspace  gdn_paged_attention_workspace_bytes, 16-byte aligned, contents irrelevant on entry;
+ *              calls that may overlap on the GPU need one each (two captured graphs included).
+ * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products
+ * with v as two bf16 terms (2^-17 relative). fp32 products are formed from split tf32 terms
+ * (about 2^-21). The result does not depend on the order in which CTAs finish.
+ * shape: B 0..65535, T 1..16, d 64, 128 or 256, H_q <= 65535.
+ */
+gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                               const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* kv_len, const int32_t* q_len, void* o, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdn_paged_attention needs (0 for an invalid shape); uses B, T, H_q, H_kv, d and
+ * dtype of the shape, and not the device. */
+size_t gdn_paged_attention_workspace_bytes(const gdn_kv_shape* shape);
 
 /* Bytes of stash gdn_verify_step writes for this shape (0 for an invalid shape). */
 size_t gdn_stash_bytes(const gdn_shape* shape);
