@@ -1,100 +1,578 @@
 // gdn_attn.cu -- attention of one new token or a verify block over the paged cache
-// (gdn_paged_attention in include/gdn.h).
+// (gdn_paged_attention in include/gdn.h): the streaming kernel, and the choice of kernel.
 //
-// One CTA per row (b, t, query head); its warps take the positions in turn, each with a running
-// maximum and sum of the softmax, and are joined in shared memory.
+// For few rows the cache is read once and each value meets a handful of queries: the kernel is a
+// stream from HBM. Every warp is a unit of its own: it fetches 16 positions at a time (keys and
+// values of one key head) into a ring in shared memory with 16-byte asynchronous copies, finding
+// each position's page itself, so pages of any size and any strides stream alike, and works on them
+// with warp matrix instructions while the next ones arrive. No barrier stands in the loop. The
+// rows of a key head (block rows x heads that share it) are the 16 rows of the matrix products:
+//   s = q k^T (base-2 exponents), running maximum m and sum l per row, o = o 2^(m - m') + 2^(s - m') v.
+// A warp's maxima, totals and sums are joined with the other warps' when the CTA leaves the item.
+//
+// Precision. bf16 products are exact in fp32. The weights 2^(s - m) enter the second product as two
+// bf16 terms (2^-17 relative), because one (2^-9) would be as large as the rounding of a bf16
+// result; the matrix units have the room. fp32 operands are split into two tf32 terms each, and the
+// three products that matter are added (2^-21). Statistics and sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "gdn_device.cuh"
-#include "gdn_internal.cuh"
+#include <algorithm>
+
+#include "gdn_attn.cuh"
 
 namespace gdn {
+namespace attn {
 namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 4;
-
+// Geometry of the streaming kernel. A stage is 16 positions of keys and values.
 template <typename E, int D>
-__global__ void __launch_bounds__(kWarps * 32) gdn_paged_attention_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int N = D / 32;
-    __shared__ float s_o[kWarps][D], s_m[kWarps], s_l[kWarps];
-    const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kv = a.kv_len[b], q_len = a.q_len ? a.q_len[b] : a.T;
-    if (kv < 0 || kv > a.max_pages * a.cache.page || q_len < 0 || q_len > a.T) {
-        if (threadIdx.x == 0 && a.status_word) atomicOr(a.status_word, kStatusBadLength);
-        return;
-    }
-    if (t >= q_len) return;
-    const int p = kv - q_len + t;
-    const int first = a.window > 0 ? max(0, p - a.window + 1) : 0;
-    const int64_t row = ((int64_t)b * a.T + t) * a.Hq + h;
-    const int64_t head = (int64_t)(h / (a.Hq / a.Hk)) * a.cache.head_stride;
-    float q[N], o[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] = ld_in<E>(a.q, row * D + i * 32 + lane) * a.scale;
-        o[i] = 0.f;
-    }
-    float m = -INFINITY, sum = 0.f;
-    for (int j = first + warp; j <= p; j += kWarps) {
-        const int id = a.table[(int64_t)b * a.max_pages + j / a.cache.page];
-        if (id < 0 || id >= a.cache.num_pages) {
-            if (lane == 0 && a.status_word) atomicOr(a.status_word, kStatusBadPage);
-            continue;
-        }
-        const int64_t at = id * a.cache.page_stride + (j % a.cache.page) * a.cache.slot_stride + head;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(q[i], ld_in<E>(a.cache.k, at + i * 32 + lane), s);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s);
-        const float use = mn == -INFINITY ? 0.f : mn;
-        const float c = expf(m - use), w = expf(s - use);
-        sum = sum * c + w;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(w, ld_in<E>(a.cache.v, at + i * 32 + lane), o[i] * c);
-        m = mn;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_o[warp][i * 32 + lane] = o[i];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = sum;
-    }
-    __syncthreads();
-    float top = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float use = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    for (int w = 0; w < kWarps; ++w) l += s_l[w] * expf(s_m[w] - use);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += s_o[w][i] * expf(s_m[w] - use);
-        if (a.out_bf16) st_out<__nv_bfloat16>(a.o, row * D + i, x * inv);
-        else st_out<float>(a.o, row * D + i, x * inv);
-    }
-    if (threadIdx.x == 0 && a.lse) a.lse[row] = use + logf(l);
+struct Geo {
+    static constexpr int kRow = D * (int)sizeof(E);              // bytes of one position
+    static constexpr int kStage = 2 * 16 * kRow;
+    static constexpr int kWarps = kStage <= 16384 ? 4 : 3;
+    static constexpr int kStages = kStage <= 4096 ? 4 : kStage <= 16384 ? 3 : 2;
+    static constexpr int kCtasPerSm = kStage <= 4096 ? 3 : kStage <= 8192 ? 2 : 1;
+    static constexpr int kUnit = 16 * kWarps;                    // positions per unit
+    static constexpr int kMaxTiles = D <= 128 ? 2 : 1;           // 16-row tiles a warp's registers hold
+    static constexpr int kRing = kStages * kStage;               // bytes per warp
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    // a source size of 0 fills the 16 bytes with zeros and reads nothing
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo with hi the leading 11 bits; lo's own tail (2^-22 of x) is left to the matrix unit.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 g = __floats2bfloat162_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&g);
+}
+
+// Where 16-byte chunk `chunk` of row `row` lies: the rows of a tile are permuted within themselves so
+// that the eight rows (bf16: one 16-byte chunk of each; fp32: two chunks of four) that a matrix
+// fragment reads at once lie in different banks.
 template <typename E>
-cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-    const dim3 grid(a.Hq, a.T, a.B);
-    if (a.d == 64) gdn_paged_attention_kernel<E, 64><<<grid, kWarps * 32, 0, stream>>>(a);
-    else if (a.d == 128) gdn_paged_attention_kernel<E, 128><<<grid, kWarps * 32, 0, stream>>>(a);
-    else gdn_paged_attention_kernel<E, 256><<<grid, kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+__device__ __forceinline__ int swizzle(int row, int chunk) {
+    if constexpr (sizeof(E) == 2) return chunk ^ (row & 7);
+    else return chunk ^ (((row ^ (row >> 2)) & 3) << 1);
+}
+template <typename E, int D>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int chunk) {
+    return base + row * (D * (int)sizeof(E)) + swizzle<E>(row, chunk) * 16;
+}
+__device__ __forceinline__ float lds(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float2 lds2(uint32_t addr) {
+    float2 x;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr) : "memory");
+    return x;
+}
+// Element (row, col) of a tile as fp32.
+template <typename E, int D>
+__device__ __forceinline__ float element(const unsigned char* tile, int row, int col) {
+    constexpr int per = 16 / sizeof(E);
+    const unsigned char* p = tile + row * (D * (int)sizeof(E)) + swizzle<E>(row, col / per) * 16 + col % per * (int)sizeof(E);
+    return to_f(*reinterpret_cast<const E*>(p));
+}
+
+template <typename E, int D>
+__device__ __forceinline__ void set_zero(unsigned char* tile, int row, int col) {
+    constexpr int per = 16 / sizeof(E);
+    unsigned char* p = tile + row * (D * (int)sizeof(E)) + swizzle<E>(row, col / per) * 16 + col % per * (int)sizeof(E);
+    *reinterpret_cast<E*>(p) = E(0.f);
+}
+
+// s[j] += q k^T for the 16 positions of a stage (j: its two halves), one 16-row tile of q.
+template <int D>
+__device__ __forceinline__ void scores(const __nv_bfloat16*, uint32_t q, uint32_t k, int lane, float (&s)[2][4]) {
+    const int row = lane & 15, half = lane >> 4;
+    const int krow = (lane & 7) + (lane >> 4) * 8, khalf = (lane >> 3) & 1;
+    float t[2][4] = {};   // odd steps: two chains of products instead of one
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t a[4], b[4];
+        ldmatrix4(chunk_at<__nv_bfloat16, D>(q, row, 2 * i + half), a);
+        ldmatrix4(chunk_at<__nv_bfloat16, D>(k, krow, 2 * i + khalf), b);
+        float(&d)[2][4] = (i & 1) ? t : s;
+        mma_bf16(d[0], a, b[0], b[1]);
+        mma_bf16(d[1], a, b[2], b[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += t[j][e];
+}
+template <int D>
+__device__ __forceinline__ void scores(const float*, uint32_t q, uint32_t k, int lane, float (&s)[2][4]) {
+    // column pairs 2 (lane % 4), + 1 of each step serve as the step's k index lane % 4 and + 4, in
+    // q and k alike
+    const int row = lane >> 2, pair = lane & 3;
+    float t[2][4] = {};
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const int chunk = 2 * i + (pair >> 1), in = (pair & 1) * 8;
+        const float2 q0 = lds2(chunk_at<float, D>(q, row, chunk) + in), q1 = lds2(chunk_at<float, D>(q, row + 8, chunk) + in);
+        uint32_t ah[4], al[4];
+        split_tf32(q0.x, ah[0], al[0]);
+        split_tf32(q1.x, ah[1], al[1]);
+        split_tf32(q0.y, ah[2], al[2]);
+        split_tf32(q1.y, ah[3], al[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 kk = lds2(chunk_at<float, D>(k, row + 8 * j, chunk) + in);
+            uint32_t bh[2], bl[2];
+            split_tf32(kk.x, bh[0], bl[0]);
+            split_tf32(kk.y, bh[1], bl[1]);
+            mma_tf32(t[j], al, bh[0], bh[1]);
+            mma_tf32(t[j], ah, bl[0], bl[1]);
+            mma_tf32(s[j], ah, bh[0], bh[1]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += t[j][e];
+}
+
+// o += p v for the 16 positions of a stage, MT row tiles (a value fragment serves all of them).
+template <int D, int MT>
+__device__ __forceinline__ void products(const __nv_bfloat16*, const float (&p)[MT][2][4], uint32_t v, int lane,
+                                         float (&o)[MT][D / 8][4]) {
+    uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            split_bf16(p[m][j][0], p[m][j][1], hi[m][2 * j], lo[m][2 * j]);
+            split_bf16(p[m][j][2], p[m][j][3], hi[m][2 * j + 1], lo[m][2 * j + 1]);
+        }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t b[4];
+        ldmatrix4_trans(chunk_at<__nv_bfloat16, D>(v, lane & 15, 2 * i + (lane >> 4)), b);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            mma_bf16(o[m][2 * i], hi[m], b[0], b[1]);
+            mma_bf16(o[m][2 * i + 1], hi[m], b[2], b[3]);
+            mma_bf16(o[m][2 * i], lo[m], b[0], b[1]);
+            mma_bf16(o[m][2 * i + 1], lo[m], b[2], b[3]);
+        }
+    }
+}
+template <int D, int MT>
+__device__ __forceinline__ void products(const float*, const float (&p)[MT][2][4], uint32_t v, int lane,
+                                         float (&o)[MT][D / 8][4]) {
+    // position pairs 2 (lane % 4), + 1 of each half serve as its k index lane % 4 and + 4
+    const int col = lane >> 2, pair = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            split_tf32(p[m][j][0], ph[m][0], pl[m][0]);
+            split_tf32(p[m][j][2], ph[m][1], pl[m][1]);
+            split_tf32(p[m][j][1], ph[m][2], pl[m][2]);
+            split_tf32(p[m][j][3], ph[m][3], pl[m][3]);
+        }
+        const int row = 8 * j + 2 * pair;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const int chunk = 2 * i + (col >> 2), in = (col & 3) * 4;
+            uint32_t bh[2], bl[2];
+            split_tf32(lds(chunk_at<float, D>(v, row, chunk) + in), bh[0], bl[0]);
+            split_tf32(lds(chunk_at<float, D>(v, row + 1, chunk) + in), bh[1], bl[1]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                mma_tf32(o[m][i], pl[m], bh[0], bh[1]);
+                mma_tf32(o[m][i], ph[m], bl[0], bl[1]);
+                mma_tf32(o[m][i], ph[m], bh[0], bh[1]);
+            }
+        }
+    }
+}
+
+// For a stage whose values are not all numbers while some row does not see all of its positions: 0
+// times infinity would reach that row in the product. So what is not a number goes straight to
+// the sums of the rows that see it, and leaves a zero in the stage; the product that follows is the
+// one the other rows would have had without it, bit for bit.
+template <typename E, int D, int MT>
+__device__ __forceinline__ void take_out_non_numbers(unsigned char* v, const uint32_t (&seen)[MT][2], int lane,
+                                                     float (&o)[MT][D / 8][4]) {
+#pragma unroll 1
+    for (int key = 0; key < 16; ++key)
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = element<E, D>(v, key, 8 * i + 2 * (lane & 3) + e);
+                if (isfinite(x)) continue;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (seen[m][0] >> key & 1) o[m][i][e] += x;
+                    if (seen[m][1] >> key & 1) o[m][i][2 + e] += x;
+                }
+            }
+    __syncwarp();
+    for (int i = lane; i < 16 * D; i += 32)
+        if (!isfinite(element<E, D>(v, i / D, i % D))) set_zero<E, D>(v, i / D, i % D);
+    __syncwarp();
+}
+
+// grid (C, row tiles). Shared memory: the warps' rings, then the CTA's 16 MT query rows.
+template <typename E, int D, int MT>
+__global__ void __launch_bounds__(Geo<E, D>::kWarps * 32, Geo<E, D>::kCtasPerSm)
+gdn_paged_attention_kernel(const __grid_constant__ Args x) {
+    using G = Geo<E, D>;
+    constexpr int NW = G::kWarps, NT = NW * 32, S = G::kStages;
+    constexpr int CPR = G::kRow / 16;                  // 16-byte chunks per position
+    constexpr int LOADS = 16 * CPR / 32;               // per lane, of keys and of values
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t s_start[NT + 2];
+    __shared__ float s_m[NW][16 * MT], s_l[NW][16 * MT];
+    const AttnArgs& a = x.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = gridDim.x, c = blockIdx.x, tile = blockIdx.y;
+    // the join kernel may take its place on the SMs now; it waits for this one to end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Start at = find_start<NT>(x, s_start, c, C, c == 0 && tile == 0);
+
+    unsigned char* ring = smem + warp * G::kRing;
+    unsigned char* q_tile = smem + NW * G::kRing;
+    const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(q_tile);
+    const int share = a.Hq / a.Hk, row0 = tile * x.rows, all_rows = share * a.T;
+    const uint32_t page = (uint32_t)a.cache.page;
+    const E* kc = static_cast<const E*>(a.cache.k);
+    const E* vc = static_cast<const E*>(a.cache.v);
+
+    int64_t u = at.u;
+    int b = at.b;
+    int64_t base = at.base;
+    while (u < at.end) {
+        bool bad;
+        Seq s = read_seq(a, G::kUnit, b, bad);
+        while (u >= base + (int64_t)s.units * a.Hk) {
+            base += (int64_t)s.units * a.Hk;
+            s = read_seq(a, G::kUnit, ++b, bad);
+        }
+        const int h = (int)((u - base) / s.units);
+        const int i0 = (int)(u - base - (int64_t)h * s.units);                 // units of the item done before
+        const int i1 = (int)min((int64_t)s.units, at.end - u + i0);
+        const bool whole = i0 == 0 && i1 == s.units;
+        const int slot = u == at.u ? 0 : 1;
+        u += i1 - i0;
+        if (row0 / share >= s.rows) continue;                                  // none of this tile's rows
+
+        // the item's query rows
+        for (int i = tid; i < 16 * MT * CPR; i += NT) {
+            const int r = i / CPR, ch = i - r * CPR, row = row0 + r;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < all_rows) {
+                const int t = row / share;
+                const int64_t qr = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
+                w = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + qr * G::kRow + ch * 16);
+            }
+            *reinterpret_cast<uint4*>(q_tile + r * G::kRow + swizzle<E>(r, ch) * 16) = w;
+        }
+        __syncthreads();
+
+        // what the rows see: row r sees lo .. p, both non-decreasing in r
+        const int p0 = s.kv - s.rows;
+        const int t_first = row0 / share, t_last = min(row0 + 16 * MT, all_rows) - 1;
+        const int p_min = p0 + t_first, lo_max = a.window > 0 ? p0 + t_last / share - a.window + 1 : 0;
+        const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
+
+        // this warp's stages: 16 positions from 16 g on, g = g_first, + NW, ... below g_end
+        const int first = s.first + i0 * G::kUnit;
+        const int g_end = min((s.first + i1 * G::kUnit) / 16, (s.kv + 15) / 16);
+        int g_load = first / 16 + warp, g = g_load;
+
+        // Lanes 0 .. 15 each look one position up: its page, its offset in the cache (-1: not there).
+        int id = -1;
+        auto look_up = [&](int gg) {
+            const int pos = gg * 16 + lane;
+            id = -1;
+            if (lane < 16 && gg < g_end && pos < s.kv && pos >= lo_min) {
+                id = a.table[(int64_t)b * a.max_pages + (uint32_t)pos / page];
+                if ((unsigned)id >= (unsigned)a.cache.num_pages) {
+                    if (a.status_word) atomicOr(a.status_word, kStatusBadPage);
+                    id = -1;
+                }
+            }
+        };
+        uint32_t there[S];           // the stage's positions that are there, one bit each
+        auto fetch = [&](int stage) -> uint32_t {
+            const uint32_t in_page = (uint32_t)(g_load * 16 + (lane & 15)) % page;
+            const int64_t off = id * a.cache.page_stride + (int64_t)in_page * a.cache.slot_stride + h * a.cache.head_stride;
+            const uint32_t mask = __ballot_sync(kFull, id >= 0);
+            const uint32_t k_at = ring_at + stage * G::kStage, v_at = k_at + G::kStage / 2;
+            if (g_load < g_end) {
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) {
+                    const int n = i * 32 + lane, row = n / CPR, ch = n - row * CPR;
+                    const int64_t o = __shfl_sync(kFull, off, row);
+                    const bool take = mask >> row & 1;
+                    const int64_t e = take ? o + ch * (16 / (int)sizeof(E)) : 0;
+                    cp_async16(chunk_at<E, D>(k_at, row, ch), kc + e, take);
+                    cp_async16(chunk_at<E, D>(v_at, row, ch), vc + e, take);
+                }
+            }
+            cp_async_commit();
+            g_load += NW;
+            look_up(g_load);
+            return mask;
+        };
+
+        float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+        }
+
+        look_up(g_load);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) there[i] = fetch(i);
+        while (g < g_end) {
+#pragma unroll
+            for (int stage = 0; stage < S; ++stage) {      // unrolled so that `there` stays in registers
+                if (g >= g_end) break;
+                there[(stage + S - 1) % S] = fetch((stage + S - 1) % S);
+                cp_async_wait<S - 1>();
+                __syncwarp();
+                const uint32_t k_at = ring_at + stage * G::kStage, v_at = k_at + G::kStage / 2;
+                const uint32_t mask = there[stage];
+                const bool all = mask == 0xffffu && g * 16 + 15 <= p_min && g * 16 >= lo_max;
+                float p[MT][2][4];
+                uint32_t seen[MT][2];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[i][j][e] = 0.f;
+                    scores<D>(static_cast<const E*>(nullptr), q_at + i * 16 * G::kRow, k_at, lane, p[i]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[i][j][e] *= x.c;
+                    if (!all) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            // bits of the positions that this row sees
+                            const int row = row0 + 16 * i + (lane >> 2) + 8 * r;
+                            const int pr = p0 + row / share;
+                            const int hi = pr - g * 16, lo = a.window > 0 ? pr - a.window + 1 - g * 16 : 0;
+                            uint32_t bits = hi < 0 ? 0u : hi >= 15 ? 0xffffu : (2u << hi) - 1u;
+                            if (lo > 0) bits = lo >= 16 ? 0u : bits & (0xffffu << lo);
+                            bits &= mask;
+                            seen[i][r] = bits;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (!(bits >> (8 * j + 2 * (lane & 3) + e) & 1)) p[i][j][2 * r + e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float top = fmaxf(fmaxf(p[i][0][2 * r], p[i][0][2 * r + 1]), fmaxf(p[i][1][2 * r], p[i][1][2 * r + 1]));
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                        if (top > m[i][r]) {
+                            const float k = exp2_approx(m[i][r] - top);     // 0 the first time
+                            m[i][r] = top;
+                            l[i][r] *= k;
+#pragma unroll
+                            for (int j = 0; j < D / 8; ++j) {
+                                o[i][j][2 * r] *= k;
+                                o[i][j][2 * r + 1] *= k;
+                            }
+                        }
+                        const float use = m[i][r] == -INFINITY ? 0.f : m[i][r];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                p[i][j][2 * r + e] = exp2_approx(p[i][j][2 * r + e] - use);
+                                l[i][r] += p[i][j][2 * r + e];
+                            }
+                    }
+                }
+                if (!all) {
+                    unsigned char* v = ring + stage * G::kStage + G::kStage / 2;
+                    bool numbers = true;
+                    for (int i = lane; i < 16 * D; i += 32) numbers &= isfinite(element<E, D>(v, i / D, i % D));
+                    if (!__all_sync(kFull, numbers)) take_out_non_numbers<E, D, MT>(v, seen, lane, o);
+                }
+                products<D, MT>(static_cast<const E*>(nullptr), p, v_at, lane, o);
+                g += NW;
+                __syncwarp();      // the stage is overwritten by the next fetch
+            }
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+
+        // The warps' results, joined through their rings.
+        float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[i][r] += __shfl_xor_sync(kFull, l[i][r], 1);
+                l[i][r] += __shfl_xor_sync(kFull, l[i][r], 2);
+                const int row = 16 * i + (lane >> 2) + 8 * r;
+                if ((lane & 3) == 0) {
+                    s_m[warp][row] = m[i][r];
+                    s_l[warp][row] = l[i][r];
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2*>(mine + row * D + 8 * j + 2 * (lane & 3)) = make_float2(o[i][j][2 * r], o[i][j][2 * r + 1]);
+            }
+        }
+        __syncthreads();
+        const size_t part = (((size_t)tile * C + c) * 2 + slot) * x.rows;
+        for (int i = tid; i < 16 * MT * (D / 4); i += NT) {
+            const int r = i / (D / 4), col = (i - r * (D / 4)) * 4, row = row0 + r, t = row / share;
+            if (row >= all_rows || t >= s.rows) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
+            const float use = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float k = exp2_approx(s_m[w][r] - use);
+                sum = fmaf(k, s_l[w][r], sum);
+                fma4(y, k, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * G::kRing) + r * D + col));
+            }
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int64_t out = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
+                store_o4(a, out * D + col, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                if (col == 0 && a.lse) a.lse[out] = (use + log2f(sum)) * kLn2;
+            } else {
+                *reinterpret_cast<float4*>(x.parts.o + (part + r) * D + col) = y;
+                if (col == 0) {
+                    x.parts.m[part + r] = top;
+                    x.parts.l[part + r] = sum;
+                }
+            }
+        }
+        __syncthreads();   // the rings and the queries are the next item's
+    }
+}
+
+// Row tiles a warp takes at once: as many as hold the rows, at most what its registers hold.
+template <typename E, int D>
+Plan plan_stream(int sms, int rows) {
+    using G = Geo<E, D>;
+    int mt = 1;
+    while (mt < G::kMaxTiles && 16 * mt < rows) mt *= 2;
+    Plan p;
+    p.unit = G::kUnit;
+    p.rows = 16 * mt;
+    p.tiles = (rows + p.rows - 1) / p.rows;
+    p.ctas = std::max(1, sms * G::kCtasPerSm / p.tiles);
+    return p;
+}
+
+template <typename E, int D, int MT>
+cudaError_t launch_stream(const Args& x, const Plan& p, cudaStream_t stream) {
+    using G = Geo<E, D>;
+    constexpr int bytes = G::kWarps * G::kRing + 16 * MT * G::kRow;
+    cudaError_t e = ensure_smem_attr<gdn_paged_attention_kernel<E, D, MT>>(bytes);
+    if (e != cudaSuccess) return e;
+    gdn_paged_attention_kernel<E, D, MT><<<dim3(p.ctas, p.tiles), G::kWarps * 32, bytes, stream>>>(x);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(x, p, stream);
+}
+
+template <typename E, int D>
+cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
+    if (p.rows == 16) return launch_stream<E, D, 1>(x, p, stream);
+    if constexpr (D <= 128)
+        if (p.rows == 32) return launch_stream<E, D, 2>(x, p, stream);
+    return cudaErrorInvalidValue;
+}
+
+Plan plan_of(int sms, int rows, int d, bool bf16) {
+    sms = std::min(sms, kMaxSms);
+    if (bf16)
+        return d == 64 ? plan_stream<__nv_bfloat16, 64>(sms, rows)
+                       : d == 128 ? plan_stream<__nv_bfloat16, 128>(sms, rows) : plan_stream<__nv_bfloat16, 256>(sms, rows);
+    return d == 64 ? plan_stream<float, 64>(sms, rows)
+                   : d == 128 ? plan_stream<float, 128>(sms, rows) : plan_stream<float, 256>(sms, rows);
 }
 
 }  // namespace
+}  // namespace attn
 
-size_t paged_attention_workspace_bytes(int, int, int, int, int, bool) { return 0; }
+size_t paged_attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, bool bf16) {
+    if (B == 0) return 0;
+    return attn::parts_bytes(attn::plan_of(attn::kMaxSms, Hq / Hk * T, d, bf16), B, d);
+}
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
-    return a.bf16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+    using namespace attn;
+    int sms = 0;
+    cudaError_t e = current_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const Plan p = plan_of(sms, a.Hq / a.Hk * a.T, a.d, a.bf16);
+    Args x;
+    x.a = a;
+    x.parts = parts_at(a.workspace, p, a.B, a.d);
+    x.rows = p.rows;
+    x.unit = p.unit;
+    x.c = a.scale * kLog2e;
+    if (a.bf16)
+        return a.d == 64 ? launch_rows<__nv_bfloat16, 64>(x, p, stream)
+                         : a.d == 128 ? launch_rows<__nv_bfloat16, 128>(x, p, stream) : launch_rows<__nv_bfloat16, 256>(x, p, stream);
+    return a.d == 64 ? launch_rows<float, 64>(x, p, stream)
+                     : a.d == 128 ? launch_rows<float, 128>(x, p, stream) : launch_rows<float, 256>(x, p, stream);
 }
 
 }  // namespace gdn
