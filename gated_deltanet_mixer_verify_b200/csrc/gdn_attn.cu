@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "gdn_attn.cuh"
+#include "gdn_attn_tc.cuh"
 
 namespace gdn {
 namespace attn {
@@ -265,14 +266,14 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
     constexpr int CPR = G::kRow / 16;                  // 16-byte chunks per position
     constexpr int LOADS = 16 * CPR / 32;               // per lane, of keys and of values
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t s_start[NT + 2];
+    __shared__ int64_t s_start[NW + 2];
     __shared__ float s_m[NW][16 * MT], s_l[NW][16 * MT];
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = gridDim.x, c = blockIdx.x, tile = blockIdx.y;
     // the join kernel may take its place on the SMs now; it waits for this one to end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    Start at = find_start<NT>(x, s_start, c, C, c == 0 && tile == 0);
+    const Start at = find_start<NT>(x, s_start, c, C, c == 0 && tile == 0);
 
     unsigned char* ring = smem + warp * G::kRing;
     unsigned char* q_tile = smem + NW * G::kRing;
@@ -282,42 +283,27 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
     const E* kc = static_cast<const E*>(a.cache.k);
     const E* vc = static_cast<const E*>(a.cache.v);
 
-    int64_t u = at.u;
-    int b = at.b;
-    int64_t base = at.base;
-    while (u < at.end) {
-        bool bad;
-        Seq s = read_seq(a, G::kUnit, b, bad);
-        while (u >= base + (int64_t)s.units * a.Hk) {
-            base += (int64_t)s.units * a.Hk;
-            s = read_seq(a, G::kUnit, ++b, bad);
-        }
-        const int h = (int)((u - base) / s.units);
-        const int i0 = (int)(u - base - (int64_t)h * s.units);                 // units of the item done before
-        const int i1 = (int)min((int64_t)s.units, at.end - u + i0);
-        const bool whole = i0 == 0 && i1 == s.units;
-        const int slot = u == at.u ? 0 : 1;
-        u += i1 - i0;
-        if (row0 / share >= s.rows) continue;                                  // none of this tile's rows
+    Walk w(at);
+    while (w.next(x)) {
+        if (row0 / share >= w.s.rows) continue;                                // none of this tile's rows
+        const Seq& s = w.s;
+        const int b = w.b, h = w.h, i0 = w.i0, i1 = w.i1;
 
         // the item's query rows
         for (int i = tid; i < 16 * MT * CPR; i += NT) {
             const int r = i / CPR, ch = i - r * CPR, row = row0 + r;
-            uint4 w = make_uint4(0, 0, 0, 0);
+            uint4 z = make_uint4(0, 0, 0, 0);
             if (row < all_rows) {
                 const int t = row / share;
                 const int64_t qr = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
-                w = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + qr * G::kRow + ch * 16);
+                z = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + qr * G::kRow + ch * 16);
             }
-            *reinterpret_cast<uint4*>(q_tile + r * G::kRow + swizzle<E>(r, ch) * 16) = w;
+            *reinterpret_cast<uint4*>(q_tile + r * G::kRow + swizzle<E>(r, ch) * 16) = z;
         }
         __syncthreads();
 
-        // what the rows see: row r sees lo .. p, both non-decreasing in r
-        const int p0 = s.kv - s.rows;
-        const int t_first = row0 / share, t_last = min(row0 + 16 * MT, all_rows) - 1;
-        const int p_min = p0 + t_first, lo_max = a.window > 0 ? p0 + t_last / share - a.window + 1 : 0;
-        const int lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
+        const Sight see(a, s, row0, min(row0 + 16 * MT, all_rows), share);
+        const int p0 = see.p0, p_min = see.p_min, lo_min = see.lo_min, lo_max = see.lo_max;
 
         // this warp's stages: 16 positions from 16 g on, g = g_first, + NW, ... below g_end
         const int first = s.first + i0 * G::kUnit;
@@ -473,23 +459,23 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
             }
         }
         __syncthreads();
-        const size_t part = (((size_t)tile * C + c) * 2 + slot) * x.rows;
+        const size_t part = (((size_t)tile * C + c) * 2 + w.slot) * x.rows;
         for (int i = tid; i < 16 * MT * (D / 4); i += NT) {
             const int r = i / (D / 4), col = (i - r * (D / 4)) * 4, row = row0 + r, t = row / share;
             if (row >= all_rows || t >= s.rows) continue;
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
+            for (int j = 0; j < NW; ++j) top = fmaxf(top, s_m[j][r]);
             const float use = top == -INFINITY ? 0.f : top;
             float sum = 0.f;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float k = exp2_approx(s_m[w][r] - use);
-                sum = fmaf(k, s_l[w][r], sum);
-                fma4(y, k, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * G::kRing) + r * D + col));
+            for (int j = 0; j < NW; ++j) {
+                const float k = exp2_approx(s_m[j][r] - use);
+                sum = fmaf(k, s_l[j][r], sum);
+                fma4(y, k, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + j * G::kRing) + r * D + col));
             }
-            if (whole) {
+            if (w.whole) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const int64_t out = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
                 store_o4(a, out * D + col, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
@@ -539,8 +525,12 @@ cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
 }
 
+// The tensor-memory kernel takes bf16 caches with more rows per key head than one 16-row tile.
+bool use_tc(int rows, bool bf16) { return bf16 && rows > 16; }
+
 Plan plan_of(int sms, int rows, int d, bool bf16) {
     sms = std::min(sms, kMaxSms);
+    if (use_tc(rows, bf16)) return plan_tc(sms, rows);
     if (bf16)
         return d == 64 ? plan_stream<__nv_bfloat16, 64>(sms, rows)
                        : d == 128 ? plan_stream<__nv_bfloat16, 128>(sms, rows) : plan_stream<__nv_bfloat16, 256>(sms, rows);
@@ -568,6 +558,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
     x.rows = p.rows;
     x.unit = p.unit;
     x.c = a.scale * kLog2e;
+    if (use_tc(a.Hq / a.Hk * a.T, a.bf16)) return launch_tc(x, p, stream);
     if (a.bf16)
         return a.d == 64 ? launch_rows<__nv_bfloat16, 64>(x, p, stream)
                          : a.d == 128 ? launch_rows<__nv_bfloat16, 128>(x, p, stream) : launch_rows<__nv_bfloat16, 256>(x, p, stream);

@@ -86,7 +86,7 @@ __device__ __forceinline__ int64_t first_unit(int64_t W, int c, int C) { return 
 __device__ __forceinline__ int cta_of(int64_t W, int64_t u, int C) { return (int)(((u + 1) * C + W - 1) / W) - 1; }
 
 // Where a CTA begins: its units [u, end), and the sequence that unit u falls into, whose units
-// begin at `base`. All NT threads call it; sm holds NT + 2 entries. CTA (0, 0) also leaves the
+// begin at `base`. All NT threads call it; sm holds NT / 32 + 2 entries. CTA (0, 0) also leaves the
 // sequences' first units for the join.
 struct Start {
     int64_t u, end, base;
@@ -137,18 +137,57 @@ __device__ __forceinline__ Start find_start(const Args& x, int64_t* sm, int c, i
             bool bad;
             const int64_t n = (int64_t)read_seq(a, x.unit, b, bad).units * a.Hk;
             if (s.u < at + n) {
-                sm[NT] = b;
-                sm[NT + 1] = at;
+                sm[NT / 32] = b;
+                sm[NT / 32 + 1] = at;
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
-    s.b = (int)sm[NT];
-    s.base = sm[NT + 1];
+    s.b = (int)sm[NT / 32];
+    s.base = sm[NT / 32 + 1];
     return s;
 }
+
+// A CTA's walk over its items: next() moves to the next (sequence, key head) and the part of its units
+// that is this CTA's. Every thread of the CTA walks alike.
+struct Walk {
+    int64_t u, begin, end, base;
+    int b, h, i0, i1;      // sequence, key head, units i0 .. i1 of the item
+    Seq s;
+    bool whole;
+    int slot;              // where a part goes
+    __device__ __forceinline__ Walk(const Start& at) : u(at.u), begin(at.u), end(at.end), base(at.base), b(at.b) {}
+    __device__ __forceinline__ bool next(const Args& x) {
+        if (u >= end) return false;
+        bool bad;
+        s = read_seq(x.a, x.unit, b, bad);
+        while (u >= base + (int64_t)s.units * x.a.Hk) {
+            base += (int64_t)s.units * x.a.Hk;
+            s = read_seq(x.a, x.unit, ++b, bad);
+        }
+        h = (int)((u - base) / s.units);
+        i0 = (int)(u - base - (int64_t)h * s.units);
+        i1 = (int)min((int64_t)s.units, end - u + i0);
+        whole = i0 == 0 && i1 == s.units;
+        slot = u == begin ? 0 : 1;
+        u += i1 - i0;
+        return true;
+    }
+};
+
+// What the rows row0 .. row1 - 1 of a sequence see (row r: positions lo .. p, both non-decreasing in
+// r): every one of them sees lo_max .. p_min, none sees below lo_min.
+struct Sight {
+    int p0, p_min, lo_min, lo_max;
+    __device__ __forceinline__ Sight(const AttnArgs& a, const Seq& s, int row0, int row1, int share) {
+        p0 = s.kv - s.rows;
+        p_min = p0 + row0 / share;
+        lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
+        lo_max = a.window > 0 ? p0 + (row1 - 1) / share - a.window + 1 : 0;
+    }
+};
 
 // The last word on one element of a row: weights w, their sum, and where it goes.
 __device__ __forceinline__ void store_o(const AttnArgs& a, int64_t at, float x) {
