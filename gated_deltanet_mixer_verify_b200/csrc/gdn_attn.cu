@@ -525,12 +525,7 @@ cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
 }
 
-// The tensor-memory kernel takes bf16 caches with more rows per key head than one 16-row tile.
-bool use_tc(int rows, bool bf16) { return bf16 && rows > 16; }
-
 Plan plan_of(int sms, int rows, int d, bool bf16) {
-    sms = std::min(sms, kMaxSms);
-    if (use_tc(rows, bf16)) return plan_tc(sms, rows);
     if (bf16)
         return d == 64 ? plan_stream<__nv_bfloat16, 64>(sms, rows)
                        : d == 128 ? plan_stream<__nv_bfloat16, 128>(sms, rows) : plan_stream<__nv_bfloat16, 256>(sms, rows);
@@ -542,8 +537,12 @@ Plan plan_of(int sms, int rows, int d, bool bf16) {
 }  // namespace attn
 
 size_t paged_attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, bool bf16) {
+    using namespace attn;
     if (B == 0) return 0;
-    return attn::parts_bytes(attn::plan_of(attn::kMaxSms, Hq / Hk * T, d, bf16), B, d);
+    const int rows = Hq / Hk * T;
+    size_t n = parts_bytes(plan_of(kMaxSms, rows, d, bf16), B, d);
+    if (bf16) n = std::max(n, parts_bytes(plan_tc(kMaxSms, rows), B, d));
+    return n;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
@@ -551,14 +550,17 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = current_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const Plan p = plan_of(sms, a.Hq / a.Hk * a.T, a.d, a.bf16);
+    sms = std::min(sms, kMaxSms);
+    const bool on_tc = tc_applies(a);
+    const int rows = a.Hq / a.Hk * a.T;
+    const Plan p = on_tc ? plan_tc(sms, rows) : plan_of(sms, rows, a.d, a.bf16);
     Args x;
     x.a = a;
     x.parts = parts_at(a.workspace, p, a.B, a.d);
     x.rows = p.rows;
     x.unit = p.unit;
     x.c = a.scale * kLog2e;
-    if (use_tc(a.Hq / a.Hk * a.T, a.bf16)) return launch_tc(x, p, stream);
+    if (on_tc) return launch_tc(x, p, stream);
     if (a.bf16)
         return a.d == 64 ? launch_rows<__nv_bfloat16, 64>(x, p, stream)
                          : a.d == 128 ? launch_rows<__nv_bfloat16, 128>(x, p, stream) : launch_rows<__nv_bfloat16, 256>(x, p, stream);

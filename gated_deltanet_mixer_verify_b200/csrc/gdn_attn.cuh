@@ -187,6 +187,8 @@ struct Sight {
         lo_min = a.window > 0 ? max(0, p_min - a.window + 1) : 0;
         lo_max = a.window > 0 ? p0 + (row1 - 1) / share - a.window + 1 : 0;
     }
+    // Whether some row does not see some of the n positions from pos on.
+    __device__ __forceinline__ bool partial(int pos, int n) const { return pos + n - 1 > p_min || pos < lo_max; }
 };
 
 // The last word on one element of a row: weights w, their sum, and where it goes.

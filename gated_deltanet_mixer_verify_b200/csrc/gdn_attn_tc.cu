@@ -3,20 +3,31 @@
 // split over CTAs).
 //
 // With T rows per sequence and H_q / H_kv heads sharing a key head, every cached value meets T H_q /
-// H_kv queries (48 for a block of 8 and 6 heads): warp matrix products in registers would be the
-// bound, or the cache would have to be read once per 16 rows. Here up to 128 rows are the M of one
-// tcgen05 product, so the cache is read once: S = Q K^T into tensor memory (128 x 64 positions), the
-// softmax on S by one thread per row (no shuffles: a row is a tensor-memory lane), its weights back into the
-// columns of S as two bf16 terms (2^-17 relative), O += P V with A from tensor memory and V as it lies
-// in the cache (positions x d, N-major). O stays in tensor memory for the whole item; a row's running
-// maximum only moves when it has grown by 2^8, so O is rescaled a few times per item, not per tile.
+// H_kv queries (48 for a block of 8 and 6 heads). Warp matrix products in registers would be the
+// bound, or the cache would have to be read once per 16 rows. Here the positions are the M of the
+// products and the rows their N, so nothing is multiplied for rows that are not there:
+//   S^T [128 positions x N rows] = K Q^T,   O^T [d x N] += V^T P^T,
+// K and V as they lie in the cache (K-major and M-major), S^T and O^T in tensor memory. A thread owns a
+// position (a lane of S^T): it masks and exponentiates its N scores and leaves the weights in shared
+// memory as two bf16 terms (2^-17 relative), the K x N operand of the second product. No
+// maximum crosses threads in the steady state: the exponents are taken against the row maxima of the
+// item's first tile, and the threads only vote whether some score has grown past them by 2^16 (fp32 and
+// bf16 have the range; nothing is lost below it), which is when maxima are taken again and O rescaled.
+// The sums of the weights stay with the threads until the item ends.
 //
-// One CTA per SM, ten warps with roles of their own: 0-3 softmax and outputs, 4-7 fetch keys and values
-// into a ring of tiles (16-byte asynchronous copies; each warp finds the pages of its 16 of a tile's
-// 64 positions, so pages of any size and any strides will do), 8 issues the products, 9 fetches
-// queries. Tiles alternate K, V in the ring; S has two buffers, so the scores of the next tile are
-// formed while this one's softmax runs, and the fetch runs ahead over the items' borders. Every wait
-// is bounded.
+// One CTA per SM with roles for its warps: softmax and outputs (four warps for each 32 rows), one that
+// fetches keys and values into a ring of [128 positions][64 columns] blocks by TMA (one copy per run
+// of a page's slots, so pages of any multiple of 8 slots and any strides will do), one that issues
+// the products, one that fetches queries and looks over the values at the ends of what the rows see.
+// The order of products, and of the ring, is K 0, K 1, V 0, K 2, V 1, ...: scores of the next tile
+// are formed before the values of this one are needed, so a block is used up as it lands, the
+// softmax runs while values land, and the whole ring is copies in flight. Every wait is bounded.
+//
+// Measured on the way (one sequence, 32K positions, 8 rows x 6 heads, d 256; 134 MB): rows as M, one thread
+// per row, P in tensor memory, 71 us; positions as M with the steps of a tile one after the other
+// (7,300 cycles per tile of 128, of which HBM needs 5,680), 68 us. A product of M 128, N 48, K 16
+// takes 48 cycles, bound by its reads of A from shared memory, and waits on barriers take 200 while
+// products run, so single steps cannot be made short; they are overlapped instead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,31 +43,32 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 320;
-constexpr int kTile = 64;                       // positions per tile, and per unit
-constexpr int kM = 128;                         // rows of a product
+constexpr int kTile = 128;                      // positions per tile, and per unit
+constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr uint32_t kMaxPolls = 1u << 22;
-constexpr float kGrow = 8.f;                    // a maximum moves when it has grown by this (base-2 exponent)
-constexpr int kMaskRing = 16;                   // more tiles than the ring and the two S buffers can hold
+constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
+constexpr int kMaskRing = 16;                   // more tiles than the ring holds, and the one in work
 
-template <int D>
+// D columns of the head, NB blocks of 64 rows.
+template <int D, int NB>
 struct Cfg {
-    static constexpr int kSlot = kTile * D * 2;                       // bytes of a K or V tile
-    static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 12 : 5;
-    // Tiles whose copies a fetching thread leaves in flight before it reports the oldest (96 to 128
-    // KB per SM; at most kSlots - 2, so that a product never waits for a tile whose report waits for
-    // the product's own slot).
-    static constexpr int kAhead = D == 64 ? 12 : D == 128 ? 8 : 3;
-    static constexpr int kQ = kM * D * 2;
-    static constexpr int kBytes = kSlots * kSlot + kQ + 1024;         // + alignment
-    static constexpr uint32_t kCols = D == 256 ? 512 : 256;           // tensor memory: S 2 x 64, O d
-    static constexpr uint32_t kO = 128;
-    static constexpr int kCpr = D / 8;                                // 16-byte chunks per position
-    static constexpr int kLoads = 16 * kCpr / 32;                     // per lane and tile
+    static constexpr int kGroups = 2 * NB;                            // of 128 threads and 32 rows
+    static constexpr int kSoft = 128 * kGroups;                       // threads of the softmax
+    static constexpr int kThreads = kSoft + 96;
+    static constexpr int kKb = D / 64;                                // ring blocks of a K or V tile
+    static constexpr int kMb = D > 128 ? D / 128 : 1;                 // M = 128 blocks of O^T
+    static constexpr int kQ = 64 * NB * D * 2;
+    static constexpr int kP = NB * kBlock;                            // one term of P
+    // even where a V operand spans two blocks, which must follow one another
+    static constexpr int kSlots = D == 256 ? (NB == 1 ? 8 : 4) : D == 128 ? (NB == 1 ? 10 : 6) : (NB == 1 ? 11 : 8);
+    static constexpr int kBytes = kSlots * kBlock + kQ + 2 * kP + 1024;   // + alignment
+    static constexpr uint32_t kO = 2 * 64 * NB;                       // column of O^T behind two S^T
+    static constexpr uint32_t kCols = 64 * NB * (2 + kMb) <= 256 ? 256 : 512;
+    static constexpr int kCpr = D / 8;                                // 16-byte chunks per row of Q
 };
 
 struct Bars {
-    uint64_t kv_full[16], kv_empty[16], s_full[2], p_full[2], pv_done[2], q_full, q_empty, o_free, drain;
+    uint64_t kv_full[16], kv_empty[16], s_full[2], p_full, pv_done, o_free, q_full, q_empty, drain;
 };
 
 // Byte offset of 16-byte chunk ch of row r in a tile of `rows` rows: blocks of 64 columns, 128-byte
@@ -65,80 +77,138 @@ __device__ __forceinline__ uint32_t tile_chunk(int rows, int r, int ch) {
     return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-    // a source size of 0 fills the 16 bytes with zeros and reads nothing
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ bool bf16_pair_not_numbers(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// The bits of those of two bf16 values that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_numbers(uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-// A wait that gives up when the CTA has been given up, or after kMaxPolls polls, and then gives the
-// CTA up.
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, volatile int* lost) {
+// Waits of a whole warp, its lanes agreeing, that give up when the CTA has been given up, or after
+// kMaxPolls polls, and then give the CTA up. First on a count in shared memory that one thread raises:
+__device__ __forceinline__ void set_count(uint32_t* count, uint32_t n) {
+    asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool await_count(uint32_t* count, uint32_t want, volatile int* lost) {
     for (uint32_t i = 0; i < kMaxPolls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        uint32_t n;
+        asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
+        if ((int32_t)(n - want) >= 0) return true;
         if (*lost) return false;
+        __nanosleep(32);
     }
     *lost = 1;
     return false;
 }
-// The same for a whole warp: its lanes agree.
+// and on a barrier:
 __device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, volatile int* lost) {
-    return __all_sync(kFull, await(bar, parity, lost));
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(kFull, *lost)) return false;
+    }
+    *lost = 1;
+    return false;
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(r));
+    return r != 0;
+}
+// Named barrier `id` over 128 threads: whether some thread says yes.
+__device__ __forceinline__ bool any128(int id, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        " .reg .pred p, q;\n"
+        " setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.or.pred q, %2, 128, p;\n"
+        " selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(r)
+        : "r"((uint32_t)yes), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
-// grid (C, row tiles of 128).
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) gdn_paged_attention_tc_kernel(const __grid_constant__ Args x) {
-    using G = Cfg<D>;
+// The maximum (or sum) over the warp's lanes of their v[c], c = 0 .. 31, halving: left in lane c.
+template <bool MAX>
+__device__ __forceinline__ float reduce32(float* v, int lane) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float send = upper ? v[i] : v[i + off], keep = upper ? v[i + off] : v[i];
+            const float other = __shfl_xor_sync(kFull, send, off);
+            v[i] = MAX ? fmaxf(keep, other) : keep + other;
+        }
+    }
+    return v[0];
+}
+
+// grid (C, row tiles of 64 NB). run: slots per copy, the largest power of two up to a tile that
+// divides the page size.
+template <int D, int NB>
+__global__ void __launch_bounds__(Cfg<D, NB>::kThreads, 1)
+gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_constant__ CUtensorMap k_map,
+                              const __grid_constant__ CUtensorMap v_map, int run) {
+    using G = Cfg<D, NB>;
+    constexpr int kSoftWarps = G::kSoft / 32;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Bars bars;
-    __shared__ int64_t s_start[kThreads / 32 + 2];
-    __shared__ alignas(8) uint16_t s_mask[kMaskRing][4];      // a tile's positions that are there, 16 for each fetching warp
-    __shared__ uint16_t s_partial[16][4];          // a V slot's positions that only some rows see
+    __shared__ int64_t s_start[G::kThreads / 32 + 2];
+    __shared__ uint32_t s_mask[kMaskRing][4];      // a tile's positions that are there
+    __shared__ float s_part[G::kGroups][4][32];    // per warp: maxima or sums of its positions
+    __shared__ alignas(16) float s_m[G::kGroups][32];  // maxima (read four at a time)
+    __shared__ alignas(16) float s_use[G::kGroups][32], s_k[G::kGroups][32];   // the same, 0 for none; factors
+    __shared__ int64_t s_row[G::kGroups][32];      // where a row goes (-1: nowhere)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_lost, s_not_numbers;
+    __shared__ uint32_t s_ask, s_looked;           // V tiles to be looked over, and looked over (counts)
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = gridDim.x, c = blockIdx.x, mtile = blockIdx.y;
     // the join kernel may take its place on the SMs now; it waits for this one to end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const uint32_t raw = smem_u32(smem_raw), base_at = (raw + 1023u) & ~1023u;
-    unsigned char* const tiles = smem_raw + (base_at - raw);
-    const uint32_t ring_at = base_at, q_at = base_at + G::kSlots * G::kSlot;
+    const uint32_t raw = smem_u32(smem_raw), ring_at = (raw + 1023u) & ~1023u;
+    unsigned char* const ring = smem_raw + (ring_at - raw);
+    constexpr uint32_t kQOff = G::kSlots * kBlock, kPOff = kQOff + G::kQ;
     if (tid == 0) {
         for (int i = 0; i < G::kSlots; ++i) {
-            mbar_init(&bars.kv_full[i], 4);
+            mbar_init(&bars.kv_full[i], 1);
             mbar_init(&bars.kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[i], 2);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.pv_done[i], 2);
-        }
+        mbar_init(&bars.s_full[0], 2);
+        mbar_init(&bars.s_full[1], 2);
+        mbar_init(&bars.p_full, kSoftWarps);
+        mbar_init(&bars.pv_done, 2);
+        mbar_init(&bars.o_free, kSoftWarps);
         mbar_init(&bars.q_full, 1);
         mbar_init(&bars.q_empty, 1);
-        mbar_init(&bars.o_free, 4);
         mbar_init(&bars.drain, 1);
         fence_barrier_init();
         s_lost = 0;
         s_not_numbers = 0;
+        s_ask = s_looked = 0;
     }
-    if (warp == 8) {
+    if (warp == kSoftWarps + 1) {
         tc::tmem_alloc(&s_tmem, G::kCols);
         tc::tmem_relinquish();
     }
     // rows of Q that are nobody's stay zero
-    for (int i = tid; i < G::kQ / 16; i += kThreads)
-        reinterpret_cast<uint4*>(tiles + G::kSlots * G::kSlot)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < G::kQ / 16; i += G::kThreads) reinterpret_cast<uint4*>(ring + kQOff)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
-    const Start at = find_start<kThreads>(x, s_start, c, C, c == 0 && mtile == 0);
+    const Start at = find_start<G::kThreads>(x, s_start, c, C, c == 0 && mtile == 0);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -148,346 +218,436 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_paged_attention_tc_kernel(con
     const int rows = min(x.rows, all_rows - row0);
     Walk w(at);
 
-    if (warp < 4) {
+    if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax and outputs
-        const int r = tid, row = row0 + r, t = row / share;
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const bool busy = warp * 32 < rows;          // some lane of this warp is a row
+        const int wg = warp >> 2, k = tid & 127, bar = 1 + wg;
+        const int my_rows = min(32, rows - 32 * wg);             // rows of this group of warps (not positive: none)
+        const int chunks = (max(my_rows, 0) + 15) / 16;          // 16 columns each
+        const int my_row0 = row0 + 32 * wg;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float cs = x.c == 0.f ? 1.f : fabsf(x.c);
-        uint32_t g = 0;                              // tiles done by this CTA
+        unsigned char* const P = ring + kPOff + (wg >> 1) * kBlock;
+        uint32_t g = 0;                                          // tiles done by this CTA
         bool fine = true;
+        float l[32];
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
-            const int p = see.p0 + t, lo = a.window > 0 ? p - a.window + 1 : 0;
-            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) l[r] = 0.f;
             for (int j = 0; j < n; ++j, ++g) {
-                const uint32_t buf = g & 1, parity = (g >> 1) & 1;
-                if (!(fine = await_warp(&bars.s_full[buf], parity, &s_lost))) break;
+                if (!(fine = await_warp(&bars.s_full[g & 1], (g >> 1) & 1, &s_lost))) break;
                 tc::fence_after_sync();
-                if (busy) {
-                    const uint32_t S = lanes + buf * kTile;
-                    float s[2][32];
-                    tc::tmem_ld32x2(S, S + 32, s[0], s[1]);
-                    if (x.c <= 0.f) {                // c is folded into the exponent as |c|
+                float s[32];
+                if (chunks > 0) {
+                    const uint32_t S = lanes + (g & 1) * (64 * NB) + 32 * wg;
+                    tc::tmem_ld16x2(S, S + 16, *reinterpret_cast<float(*)[16]>(s), *reinterpret_cast<float(*)[16]>(s + 16));
+                    if (x.c <= 0.f) {                            // c enters the exponents as |c|
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            s[0][i] = x.c < 0.f ? -s[0][i] : 0.f;
-                            s[1][i] = x.c < 0.f ? -s[1][i] : 0.f;
-                        }
+                        for (int r = 0; r < 32; ++r) s[r] = x.c < 0.f ? -s[r] : 0.f;
                     }
-                    const uint64_t mask = *reinterpret_cast<const volatile uint64_t*>(s_mask[g % kMaskRing]);
-                    const int pos = first + j * kTile;
-                    if (mask != ~0ull || pos + kTile - 1 > see.p_min || pos < see.lo_max) {
-                        const int hi = p - pos, low = lo - pos;
-                        uint64_t bits = hi < 0 ? 0ull : hi >= 63 ? ~0ull : (2ull << hi) - 1;
-                        if (low > 0) bits = low >= 64 ? 0ull : bits & (~0ull << low);
-                        bits &= mask;
+                    const int pos = first + j * kTile + k;
+                    const uint32_t mask = *const_cast<const volatile uint32_t*>(&s_mask[g % kMaskRing][warp & 3]);
+                    if (mask != ~0u || see.partial(first + j * kTile, kTile)) {
+                        // this position is seen by the rows from .. to - 1: row r stands at p0 + r / share
+                        const int64_t from = (int64_t)max(0, pos - see.p0) * share - my_row0;
+                        const int64_t to = !(mask >> lane & 1) ? from : a.window > 0 ? ((int64_t)pos - see.p0 + a.window) * share - my_row0 : 32;
+                        const int f = (int)max((int64_t)-1, min(from, (int64_t)32)), e = (int)max((int64_t)-1, min(to, (int64_t)32));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (!((uint32_t)bits >> i & 1)) s[0][i] = -INFINITY;
-                            if (!((uint32_t)(bits >> 32) >> i & 1)) s[1][i] = -INFINITY;
-                        }
+                        for (int r = 0; r < 32; ++r)
+                            if (r < f || r >= e) s[r] = -INFINITY;
                     }
-                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    bool move = j == 0;
+                    if (j > 0) {
+                        float over = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], fmaxf(s[0][i], s[1][i]));
-                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * cs;
-                    const bool grew = top > m + kGrow;
-                    if (__any_sync(kFull, grew)) {
-                        const float k = grew ? exp2_approx(m - top) : 1.f;      // 0 the first time
-                        if (grew) m = top;
-                        l *= k;
-                        if (j > 0) {
-                            if (!(fine = await_warp(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &s_lost))) break;
-                            tc::fence_after_sync();
-#pragma unroll 1
-                            for (int i = 0; i < D; i += 32) {
-                                float o[2][16];
-                                tc::tmem_ld16x2(lanes + G::kO + i, lanes + G::kO + i + 16, o[0], o[1]);
+                        for (int r = 0; r < 32; r += 4) {
+                            if (r >= 16 && chunks < 2) break;
+                            const float4 m = *reinterpret_cast<const float4*>(&s_m[wg][r]);
+                            over = fmaxf(over, fmaxf(fmaxf(fmaf(s[r], cs, -m.x), fmaf(s[r + 1], cs, -m.y)),
+                                                     fmaxf(fmaf(s[r + 2], cs, -m.z), fmaf(s[r + 3], cs, -m.w))));
+                        }
+                        move = any128(bar, over > kGrow);
+                    }
+                    if (move) {
+                        float top[32];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    o[0][e] *= k;
-                                    o[1][e] *= k;
-                                }
-                                tc::tmem_st16_nowait(lanes + G::kO + i, o[0]);
-                                tc::tmem_st16_nowait(lanes + G::kO + i + 16, o[1]);
+                        for (int r = 0; r < 32; ++r) top[r] = s[r];
+                        s_part[wg][warp & 3][lane] = reduce32<true>(top, lane);
+                        named_barrier_sync(bar, 128);
+                        if (k < 32) {
+                            float m = fmaxf(fmaxf(s_part[wg][0][k], s_part[wg][1][k]), fmaxf(s_part[wg][2][k], s_part[wg][3][k])) * cs;
+                            if (j > 0) {
+                                const float old = s_m[wg][k];
+                                m = fmaxf(m, old);
+                                s_k[wg][k] = m == old ? 1.f : exp2_approx(old - m);
                             }
-                            tc::tmem_st_wait();
+                            s_m[wg][k] = m;
+                            s_use[wg][k] = m == -INFINITY ? 0.f : m;
                         }
+                        named_barrier_sync(bar, 128);
                     }
-                    const float use = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    float hi[32], lw[32];            // bf16 pairs: columns of P's two terms
+                    // the product of the tile before still reads P, and O is rescaled behind it
+                    if (j > 0 && !(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) break;
+                    if (move && j > 0) {
+                        tc::fence_after_sync();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int half = i >> 4, e = 2 * (i & 15);
-                        const float y0 = exp2_approx(fmaf(s[half][e], cs, -use));
-                        const float y1 = exp2_approx(fmaf(s[half][e + 1], cs, -use));
-                        sum[i & 3] += y0 + y1;
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-                        const float2 f = __bfloat1622float2(h2);
-                        const __nv_bfloat162 l2 = __floats2bfloat162_rn(y0 - f.x, y1 - f.y);
-                        hi[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
-                        lw[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&l2));
+                        for (int r = 0; r < 32; ++r) l[r] *= s_k[wg][r];
+#pragma unroll 1
+                        for (int i = 0; i < G::kMb * 2; ++i) {
+                            const uint32_t O = lanes + G::kO + (i >> 1) * (64 * NB) + 32 * wg + (i & 1) * 16;
+                            float o[16];
+                            tc::tmem_ld16(O, o);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) o[r] *= s_k[wg][(i & 1) * 16 + r];
+                            tc::tmem_st16_nowait(O, o);
+                        }
+                        tc::tmem_st_wait();
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc::tmem_st32(S, hi);
-                    tc::tmem_st32(S + 32, lw);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {                // eight rows: one 16-byte chunk of each term
+                        if (q >= 2 * chunks) break;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 8 * q + 2 * e;
+                            const float2 m = *reinterpret_cast<const float2*>(&s_use[wg][r]);
+                            const float y0 = exp2_approx(fmaf(s[r], cs, -m.x)), y1 = exp2_approx(fmaf(s[r + 1], cs, -m.y));
+                            l[r] += y0;
+                            l[r + 1] += y1;
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+                            const float2 f = __bfloat1622float2(h2);
+                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(y0 - f.x, y1 - f.y);
+                            hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                            lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
+                        }
+                        const uint32_t to_chunk = tile_chunk(kTile, k, (wg & 1) * 4 + q);
+                        *reinterpret_cast<uint4*>(P + to_chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(P + G::kP + to_chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    tc::fence_proxy_async_smem();
+                } else if (j > 0 && !(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) {
+                    break;
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[buf]);
+                if (lane == 0) mbar_arrive(&bars.p_full);
             }
             if (!fine) break;
-            if (!(fine = await_warp(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &s_lost))) break;
+            // the sums, and where the rows go
+            if (chunks > 0) {
+                s_part[wg][warp & 3][lane] = reduce32<false>(l, lane);
+                named_barrier_sync(bar, 128);
+                if (k < 32) {
+                    const int row = my_row0 + k, t = row / share;
+                    const float sum = (s_part[wg][0][k] + s_part[wg][1][k]) + (s_part[wg][2][k] + s_part[wg][3][k]);
+                    int64_t to = -1;
+                    if (k < my_rows && t < w.s.rows) {
+                        if (w.whole) {
+                            to = ((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + (row - t * share);
+                            if (a.lse) a.lse[to] = (s_use[wg][k] + log2f(sum)) * kLn2;
+                        } else {
+                            to = (((int64_t)mtile * C + c) * 2 + w.slot) * x.rows + 32 * wg + k;
+                            x.parts.m[to] = s_m[wg][k];
+                            x.parts.l[to] = sum;
+                        }
+                    }
+                    s_row[wg][k] = to;
+                    s_k[wg][k] = !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                }
+                named_barrier_sync(bar, 128);
+            }
+            if (!(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) break;
             tc::fence_after_sync();
-            if (busy) {
-                const bool mine = r < rows && t < w.s.rows;
+            if (chunks > 0) {
                 const bool repair = s_not_numbers != 0;
-                const float inv = w.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const int64_t out = ((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + (row - t * share);
-                const size_t part = (((size_t)mtile * C + c) * 2 + w.slot) * x.rows + r;
 #pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    float o[2][16];
-                    tc::tmem_ld16x2(lanes + G::kO + i, lanes + G::kO + i + 16, o[0], o[1]);
-                    if (!mine) continue;
+                for (int i = 0; i < G::kMb * chunks; ++i) {
+                    const int mb = i / chunks, q = i - mb * chunks, col = mb * 128 + k;
+                    float o[16];
+                    tc::tmem_ld16(lanes + G::kO + mb * (64 * NB) + 32 * wg + q * 16, o);
+                    if (col >= D) continue;                      // d = 64: the upper lanes hold it twice
                     if (repair) {
-                        // what was taken out of the tiles (see the fetch): to the rows that see it
+                        // what was taken out of the tiles (see the look below): to the rows that see it
                         const int end = min(w.s.kv, first + n * kTile);
                         for (int pos = max(first, see.lo_min); pos < end; ++pos) {
-                            if (pos >= see.lo_max && pos <= see.p_min) {
-                                pos = max(pos, min(see.p_min, end - 1));   // every row sees these: nothing was taken out
-                                continue;
-                            }
-                            if (pos > p || pos < lo) continue;
+                            if (pos >= see.lo_max && pos <= see.p_min) continue;   // seen by all: nothing was taken out
                             const int id = a.table[(int64_t)w.b * a.max_pages + pos / a.cache.page];
                             if ((unsigned)id >= (unsigned)a.cache.num_pages) continue;
-                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.cache.v) + id * a.cache.page_stride +
-                                                     (int64_t)(pos % a.cache.page) * a.cache.slot_stride +
-                                                     w.h * a.cache.head_stride + i;
+                            const float y = __bfloat162float(
+                                static_cast<const __nv_bfloat16*>(a.cache.v)[id * a.cache.page_stride + (int64_t)(pos % a.cache.page) * a.cache.slot_stride +
+                                                                             w.h * a.cache.head_stride + col]);
+                            if (isfinite(y)) continue;
+                            const int64_t from = (int64_t)max(0, pos - see.p0) * share - my_row0 - q * 16;
+                            const int64_t to = a.window > 0 ? ((int64_t)pos - see.p0 + a.window) * share - my_row0 - q * 16 : 16;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = __bfloat162float(v[e]);
-                                if (!isfinite(y)) o[e >> 4][e & 15] += y;
-                            }
+                            for (int r = 0; r < 16; ++r)
+                                if (r >= from && r < to) o[r] += y;
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 y = make_float4(o[e >> 4][e & 15] * inv, o[e >> 4][(e & 15) + 1] * inv,
-                                                     o[e >> 4][(e & 15) + 2] * inv, o[e >> 4][(e & 15) + 3] * inv);
-                        if (w.whole) store_o4(a, out * D + i + e, y);
-                        else *reinterpret_cast<float4*>(x.parts.o + part * D + i + e) = y;
+                    for (int r = 0; r < 16; ++r) {
+                        const int64_t to = s_row[wg][q * 16 + r];
+                        if (to < 0) continue;
+                        if (w.whole) store_o(a, to * D + col, o[r] * s_k[wg][q * 16 + r]);
+                        else x.parts.o[to * D + col] = o[r];
                     }
                 }
-                if (mine) {
-                    if (!w.whole) {
-                        x.parts.m[part] = m;
-                        x.parts.l[part] = l;
-                    } else if (a.lse) {
-                        a.lse[out] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-                    }
-                }
+                named_barrier_sync(bar, 128);                    // s_row, s_k and s_part are the next item's
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);
         }
-    } else if (warp < 8) {
+    } else if (warp == kSoftWarps) {
         // ---------------------------------------------------------------- keys and values
-        const int fw = warp - 4;                     // this warp's 16 positions of a tile
-        const uint32_t page = (uint32_t)a.cache.page;
-        const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.cache.k);
-        const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.cache.v);
-        uint32_t issued = 0, told = 0, g = 0;        // tiles of the ring issued and reported, position tiles
-        // Reports the oldest tile whose copies have landed. Values that are not numbers at positions
-        // that some row does not see would reach it as 0 times infinity: they leave a zero, and the rows
-        // that do see them get them at the end (`repair` above).
-        auto tell = [&]() {
-            const uint32_t slot = told % G::kSlots;
-            const uint32_t partial = s_partial[slot][fw];
-            if (partial) {
-#pragma unroll 1
-                for (int i = 0; i < G::kLoads; ++i) {
-                    const int k = i * 32 + lane, pr = k / G::kCpr, ch = k - pr * G::kCpr;
-                    if (!(partial >> pr & 1)) continue;
-                    uint32_t* q = reinterpret_cast<uint32_t*>(tiles + slot * G::kSlot + tile_chunk(kTile, fw * 16 + pr, ch));
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t y = q[e];
-                        if (bf16_pair_not_numbers(y)) {
-                            s_not_numbers = 1;
-                            q[e] = ((y & 0x7f80u) == 0x7f80u ? 0u : y & 0xffffu) |
-                                   ((y & 0x7f800000u) == 0x7f800000u ? 0u : y & 0xffff0000u);
-                        }
-                    }
-                }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.kv_full[slot]);
-            ++told;
-        };
+        const int page = a.cache.page, runs = kTile / run;
+        uint32_t issued = 0, g = 0;                  // blocks of the ring, tiles
         bool fine = true;
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
-            const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile + fw * 16;
-            // Lanes 0 .. 15 each look one position up, a tile ahead: its page, -1 where it is not there.
-            int id = -1;
-            auto look_up = [&](int j) {
-                const int pos = first + j * kTile + lane;
-                id = -1;
-                if (lane < 16 && j < n && pos < w.s.kv && pos >= see.lo_min) {
-                    id = a.table[(int64_t)w.b * a.max_pages + (uint32_t)pos / page];
-                    if ((unsigned)id >= (unsigned)a.cache.num_pages) {
-                        if (a.status_word) atomicOr(a.status_word, kStatusBadPage);
-                        id = -1;
-                    }
-                }
+            const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
+            // Lane i looks up the page of run i; num_pages (which TMA reads as zeros) where nothing of it is
+            // seen or its page is not in the pool.
+            auto look_up = [&](int j) -> int {
+                const int pos = first + j * kTile + lane * run;
+                if (lane >= runs || j >= n || pos >= w.s.kv || pos + run <= see.lo_min) return a.cache.num_pages;
+                const int id = a.table[(int64_t)w.b * a.max_pages + pos / page];
+                if ((unsigned)id < (unsigned)a.cache.num_pages) return id;
+                if (a.status_word) atomicOr(a.status_word, kStatusBadPage);
+                return a.cache.num_pages;
             };
-            look_up(0);
-            for (int j = 0; j < n; ++j, ++g) {
-                const int pos = first + j * kTile + (lane & 15);
-                const int64_t off = id * a.cache.page_stride + (int64_t)((uint32_t)pos % page) * a.cache.slot_stride +
-                                    w.h * a.cache.head_stride;
-                const uint32_t mask = __ballot_sync(kFull, id >= 0);
-                const uint32_t partial = __ballot_sync(kFull, id >= 0 && (pos > see.p_min || pos < see.lo_max));
-                look_up(j + 1);
-                // K, then V; the offsets fit one shuffle each
+            auto fetch = [&](const CUtensorMap* map, int j, int id) -> bool {
+                const int slot0 = (first + j * kTile + lane * run) % page;
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
+                for (int i = 0; i < G::kKb; ++i) {
                     const uint32_t slot = issued % G::kSlots, round = issued / G::kSlots;
-                    if (!(fine = await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, &s_lost))) break;
-                    if (lane == 0) {
-                        s_partial[slot][fw] = kv ? (uint16_t)partial : (uint16_t)0;
-                        if (!kv) s_mask[g % kMaskRing][fw] = (uint16_t)mask;
+                    if (!await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, &s_lost)) return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], kBlock);
+                    __syncwarp();
+                    if (lane < runs) tc::tma_load_4d(ring + slot * kBlock + lane * run * 128, map, i * 64, w.h, slot0, id, &bars.kv_full[slot]);
+                    ++issued;
+                }
+                return true;
+            };
+            // K 0, K 1, V 0, K 2, V 1, ...; pages are looked up a tile ahead of their use
+            int id_v = a.cache.num_pages, id_k = look_up(0), id_next = look_up(1);
+            for (int j = 0; j <= n; ++j) {
+                if (j < n) {
+                    // the tile's positions that are there, 32 to a word
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int bit = lane * run - 32 * q;     // this lane's run within the word
+                        uint32_t bits = 0;
+                        if (lane < runs && id_k < a.cache.num_pages && bit < 32 && bit + run > 0)
+                            bits = run >= 32 ? ~0u : ((1u << run) - 1) << bit;
+                        bits = __reduce_or_sync(kFull, bits);
+                        if (lane == 0) s_mask[g % kMaskRing][q] = bits;
+                    }
+                    ++g;
+                    if (!(fine = fetch(&k_map, j, id_k))) break;
+                }
+                if (j > 0 && !(fine = fetch(&v_map, j - 1, id_v))) break;
+                id_v = id_k;
+                id_k = id_next;
+                id_next = look_up(j + 2);
+            }
+        }
+        if (!fine) {
+            // given up: let the copies in flight land before the shared memory goes
+            for (uint32_t s = issued > G::kSlots ? issued - G::kSlots : 0; s < issued; ++s)
+                for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.kv_full[s % G::kSlots], (s / G::kSlots) & 1); ++i) {}
+        }
+    } else if (warp == kSoftWarps + 1) {
+        // ---------------------------------------------------------------- products
+        // The whole warp walks and waits alike and one elected lane issues: what the products take (addresses,
+        // descriptors) is then the same in every lane by construction, and stays in uniform registers. A
+        // single lane's own branch cost 90 to 140 cycles per product of 25.
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        const uint32_t N = (uint32_t)(rows + 15) / 16 * 16;
+        const uint32_t id_s = tc::idesc_bf16(kTile, N, false), id_o = tc::idesc_bf16(128, N, true);
+        uint32_t g = 0, items = 0, looked = 0;
+        uint32_t slot = 0, phase = 0;                            // of the ring: the next block
+        bool fine = true;
+        while (fine && w.next(x)) {
+            if (row0 / share >= w.s.rows) continue;
+            const Sight see(a, w.s, row0, row0 + rows, share);
+            const int n = __shfl_sync(kFull, w.i1 - w.i0, 0), first = __shfl_sync(kFull, w.s.first + w.i0 * kTile, 0);
+            if (!(fine = await_warp(&bars.q_full, items & 1, &s_lost))) break;
+            // S^T = K Q^T of tile j: into the buffer that tile j - 2's reader has left
+            auto score = [&](int j) -> bool {
+                const uint32_t buf = (g + j) & 1;
+#pragma unroll 1
+                for (int kb = 0; kb < G::kKb; ++kb) {
+                    if (!await_warp(&bars.kv_full[slot], phase, &s_lost)) return false;
+                    tc::fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t k_at = ring_at + slot * kBlock, q_at = ring_at + kQOff + kb * (64 * NB * 128);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc::mma_bf16_ss(tm + buf * (64 * NB), tc::desc_kmajor_sw128(k_at + i * 32), tc::desc_kmajor_sw128(q_at + i * 32),
+                                            id_s, kb > 0 || i > 0);
+                        tc::mma_commit(&bars.kv_empty[slot]);
+                        if (kb == G::kKb - 1) {
+                            if (j == n - 1) tc::mma_commit(&bars.q_empty);
+                            tc::mma_commit(&bars.s_full[buf]);
+                            mbar_arrive(&bars.s_full[buf]);      // and what this warp has seen, the tile's mask among it
+                        }
                     }
                     __syncwarp();
-                    const __nv_bfloat16* from = kv ? vc : kc;
-                    const uint32_t to = ring_at + slot * G::kSlot;
+                    if (++slot == G::kSlots) slot = 0, phase ^= 1;
+                }
+                return true;
+            };
+            if (!(fine = score(0))) break;
+            for (int j = 0; j < n; ++j) {
+                if (j + 1 < n && !(fine = score(j + 1))) break;
+                // O^T += V^T P^T
+                if (!(fine = await_warp(&bars.p_full, (g + j) & 1, &s_lost))) break;
+                if (j == 0 && items > 0 && !(fine = await_warp(&bars.o_free, (items - 1) & 1, &s_lost))) break;
+                if (see.partial(first + j * kTile, kTile)) {
+                    uint32_t sl = slot, ph = phase;
+                    for (int kb = 0; kb < G::kKb && fine; ++kb) {
+                        fine = await_warp(&bars.kv_full[sl], ph, &s_lost);
+                        if (++sl == G::kSlots) sl = 0, ph ^= 1;
+                    }
+                    if (!fine) break;
+                    ++looked;
+                    if (lane == 0) set_count(&s_ask, looked);
+                    if (!(fine = __all_sync(kFull, await_count(&s_looked, looked, &s_lost)))) break;
+                }
+                constexpr int per = G::kKb / G::kMb;             // blocks of 64 columns per product: 2, or 1 (d = 64)
+#pragma unroll 1
+                for (int mb = 0; mb < G::kMb; ++mb) {
+                    if (!(fine = await_warp(&bars.kv_full[slot], phase, &s_lost))) break;
+                    if (per == 2 && !(fine = await_warp(&bars.kv_full[slot + per - 1], phase, &s_lost))) break;
+                    tc::fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t v_at = ring_at + slot * kBlock;
 #pragma unroll
-                    for (int i = 0; i < G::kLoads; ++i) {
-                        const int k = i * 32 + lane, pr = k / G::kCpr, ch = k - pr * G::kCpr;
-                        const int64_t o = __shfl_sync(kFull, off, pr);
-                        const bool take = mask >> pr & 1;
-                        cp_async16(to + tile_chunk(kTile, fw * 16 + pr, ch), from + (take ? o + ch * 8 : 0), take);
+                        for (int i = 0; i < 2 * kTile / 16; ++i)   // the leading term of P, then the other
+                            // d = 64: the second 64 rows of M are the first again (a stride of 0)
+                            tc::mma_bf16_ss(tm + G::kO + mb * (64 * NB), tc::desc_mnmajor_sw128(v_at + (i & 7) * 2048, per == 2 ? kBlock : 0),
+                                            tc::desc_mnmajor_sw128(ring_at + kPOff + (i >> 3) * G::kP + (i & 7) * 2048, kBlock), id_o,
+                                            j > 0 || i > 0);
+                        tc::mma_commit(&bars.kv_empty[slot]);
+                        if (per == 2) tc::mma_commit(&bars.kv_empty[slot + per - 1]);
+                        if (mb == G::kMb - 1) {
+                            tc::mma_commit(&bars.pv_done);
+                            mbar_arrive(&bars.pv_done);
+                        }
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (++issued - told > G::kAhead) {
-                        cp_async_wait<G::kAhead>();
-                        tell();
-                    }
+                    __syncwarp();
+                    slot += per;
+                    if (slot == G::kSlots) slot = 0, phase ^= 1;
                 }
                 if (!fine) break;
             }
+            g += n;
+            ++items;
         }
-        cp_async_wait<0>();
-        if (fine)
-            while (told < issued) tell();
-    } else if (warp == 8) {
-        // ---------------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t id_s = tc::idesc_bf16(kM, kTile, false), id_o = tc::idesc_bf16(kM, D, true);
-            uint32_t g = 0, items = 0;
-            bool fine = true;
-            auto score = [&](uint32_t gg, bool last) -> bool {
-                const uint32_t buf = gg & 1, s = 2 * gg, slot = s % G::kSlots;
-                // S's columns are free once the product with the weights in them is done
-                if (gg >= 2 && !await(&bars.pv_done[buf], ((gg - 2) >> 1) & 1, &s_lost)) return false;
-                if (!await(&bars.kv_full[slot], (s / G::kSlots) & 1, &s_lost)) return false;
-                tc::fence_after_sync();
-                const uint32_t k_at = ring_at + slot * G::kSlot;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    tc::mma_bf16_ss(tmem + buf * kTile, tc::desc_kmajor_sw128(q_at + (i >> 2) * (kM * 128) + (i & 3) * 32),
-                                    tc::desc_kmajor_sw128(k_at + (i >> 2) * (kTile * 128) + (i & 3) * 32), id_s, i > 0);
-                tc::mma_commit(&bars.kv_empty[slot]);
-                if (last) tc::mma_commit(&bars.q_empty);
-                tc::mma_commit(&bars.s_full[buf]);
-                mbar_arrive(&bars.s_full[buf]);      // and what this thread has seen, the tile's mask among it
-                return true;
-            };
-            while (fine && w.next(x)) {
-                if (row0 / share >= w.s.rows) continue;
-                const int n = w.i1 - w.i0;
-                if (!(fine = await(&bars.q_full, items & 1, &s_lost))) break;
-                if (!(fine = score(g, n == 1))) break;
-                for (int j = 0; j < n; ++j, ++g) {
-                    if (j + 1 < n && !(fine = score(g + 1, j + 2 == n))) break;
-                    const uint32_t buf = g & 1, s = 2 * g + 1, slot = s % G::kSlots;
-                    if (!(fine = await(&bars.p_full[buf], (g >> 1) & 1, &s_lost))) break;
-                    if (!(fine = await(&bars.kv_full[slot], (s / G::kSlots) & 1, &s_lost))) break;
-                    if (j == 0 && items > 0 && !(fine = await(&bars.o_free, (items - 1) & 1, &s_lost))) break;
-                    tc::fence_after_sync();
-                    const uint32_t v_at = ring_at + slot * G::kSlot, P = tmem + buf * kTile;
-#pragma unroll
-                    for (int i = 0; i < 2 * kTile / 16; ++i)       // the leading term of P, then the other
-                        tc::mma_bf16_ts(tmem + G::kO, P + i * 8, tc::desc_mnmajor_sw128(v_at + (i & 3) * 2048, kTile * 128),
-                                        id_o, j > 0 || i > 0);
-                    tc::mma_commit(&bars.kv_empty[slot]);
-                    tc::mma_commit(&bars.pv_done[buf]);
-                    mbar_arrive(&bars.pv_done[buf]);
-                }
-                ++items;
-            }
-            if (!fine) {
-                // given up: let the products in flight end before the tensor memory goes
-                tc::mma_commit(&bars.drain);
-                for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.drain, 0); ++i) {}
-            }
+        if (!fine && elect_one()) {
+            // given up: let the products in flight end before the tensor memory goes
+            tc::mma_commit(&bars.drain);
+            for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.drain, 0); ++i) {}
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------------------------- queries
-        uint32_t items = 0;
-        while (w.next(x)) {
+        // ---------------------------------------------------------------- queries, and values at the ends
+        uint32_t items = 0, block0 = 0, looked = 0;              // block0: the item's first block of the ring
+        bool fine = true;
+        while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
-            if (items > 0 && !await_warp(&bars.q_empty, (items - 1) & 1, &s_lost)) break;
+            const Sight see(a, w.s, row0, row0 + rows, share);
+            const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
+            if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, &s_lost))) break;
             for (int i = lane; i < rows * G::kCpr; i += 32) {
                 const int r = i / G::kCpr, ch = i - r * G::kCpr, row = row0 + r, t = row / share;
                 const int64_t qr = ((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + (row - t * share);
-                cp_async16(q_at + tile_chunk(kM, r, ch), static_cast<const __nv_bfloat16*>(a.q) + qr * D + ch * 8, true);
+                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), static_cast<const __nv_bfloat16*>(a.q) + qr * D + ch * 8);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            cp_async_wait<0>();
+            cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_full);
             ++items;
+            // Values that are not numbers, at positions that some row does not see, would reach that row
+            // as 0 times infinity. They leave a zero in the tile; the rows that do see them get them at
+            // the end (`repair` above).
+            for (int j = 0; j < n; ++j) {
+                const int pos = first + j * kTile;
+                if (!see.partial(pos, kTile)) continue;
+                if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, &s_lost)))) break;
+                const uint32_t block = block0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kKb;   // V's first block
+                for (int i = lane; i < kTile * G::kCpr; i += 32) {
+                    const int r = i / G::kCpr, ch = i - r * G::kCpr;
+                    if (pos + r <= see.p_min && pos + r >= see.lo_max) continue;
+                    uint4* q = reinterpret_cast<uint4*>(ring + (block + (ch >> 3)) % G::kSlots * kBlock + tile_chunk(kTile, r, ch & 7));
+                    uint4 y = *q;
+                    if (!(not_numbers(y.x) | not_numbers(y.y) | not_numbers(y.z) | not_numbers(y.w))) continue;
+                    s_not_numbers = 1;
+                    y.x &= ~not_numbers(y.x);
+                    y.y &= ~not_numbers(y.y);
+                    y.z &= ~not_numbers(y.z);
+                    y.w &= ~not_numbers(y.w);
+                    *q = y;
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) set_count(&s_looked, looked);
+            }
+            block0 += 2 * n * G::kKb;
         }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 8) tc::tmem_dealloc(tmem, G::kCols);
+    if (warp == kSoftWarps + 1) tc::tmem_dealloc(tmem, G::kCols);
     if (tid == 0 && s_lost && a.status_word) atomicOr(a.status_word, kStatusWaitTimeout);
 }
 
-template <int D>
+template <int D, int NB>
 cudaError_t launch(const Args& x, const Plan& p, cudaStream_t stream) {
-    cudaError_t e = ensure_smem_attr<gdn_paged_attention_tc_kernel<D>>(Cfg<D>::kBytes);
+    using G = Cfg<D, NB>;
+    static_assert(G::kBytes + 6144 <= 227 * 1024, "shared memory");
+    const PagedCache& c = x.a.cache;
+    const int run = std::min(kTile, c.page & -c.page);
+    CUtensorMap maps[2];
+    cudaError_t e = ensure_smem_attr<gdn_paged_attention_tc_kernel<D, NB>>(G::kBytes);
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = tc::encode_tmap_paged(&maps[i], i ? c.v : c.k, D, x.a.Hk, c.page, c.num_pages, c.head_stride, c.slot_stride,
+                                  c.page_stride, run);
     if (e != cudaSuccess) return e;
-    gdn_paged_attention_tc_kernel<D><<<dim3(p.ctas, p.tiles), kThreads, Cfg<D>::kBytes, stream>>>(x);
+    gdn_paged_attention_tc_kernel<D, NB><<<dim3(p.ctas, p.tiles), G::kThreads, G::kBytes, stream>>>(x, maps[0], maps[1], run);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join(x, p, stream);
+}
+template <int D>
+cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
+    return p.rows <= 64 ? launch<D, 1>(x, p, stream) : launch<D, 2>(x, p, stream);
 }
 
 }  // namespace
 
+bool tc_applies(const AttnArgs& a) {
+    const int64_t most = ((int64_t)1 << 39) - 1;      // elements: strides of a tensor map are below 2^40 bytes
+    return a.bf16 && a.Hq / a.Hk * a.T > 16 && a.cache.page % 8 == 0 && a.cache.page_stride <= most &&
+           a.cache.slot_stride <= most && a.cache.head_stride <= most;
+}
+
 Plan plan_tc(int sms, int rows) {
     Plan p;
     p.unit = kTile;
-    p.rows = std::min(rows, kM);
-    p.tiles = (rows + kM - 1) / kM;
+    p.rows = std::min(rows, 128);
+    p.tiles = (rows + 127) / 128;
     p.ctas = std::max(1, sms / p.tiles);
     return p;
 }
 
 cudaError_t launch_tc(const Args& x, const Plan& p, cudaStream_t stream) {
-    return x.a.d == 64 ? launch<64>(x, p, stream) : x.a.d == 128 ? launch<128>(x, p, stream) : launch<256>(x, p, stream);
+    return x.a.d == 64 ? launch_rows<64>(x, p, stream) : x.a.d == 128 ? launch_rows<128>(x, p, stream) : launch_rows<256>(x, p, stream);
 }
 
 }  // namespace attn

@@ -51,10 +51,10 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint3
            ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, bf16 A (K-major) and bf16 B
-// (K-major, or MN-major), shape M x N.
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool b_mn_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, bf16 A and B, both K-major or
+// both MN-major, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool mn_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((mn_major ? 3u : 0u) << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16, issued by one thread.
@@ -67,20 +67,6 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
         "}\n" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16 (A row m in lane m, elements 2 c and 2 c + 1 in
-// column a_tmem + c), issued by one thread.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 
@@ -296,6 +282,14 @@ cudaError_t encode_tmap_f32_sw128(CUtensorMap* map, const void* base, uint64_t r
 // read as zero. d * element size must be a multiple of 16 bytes and d <= 256.
 cudaError_t encode_tmap_tokens(CUtensorMap* map, const void* base, bool bf16, uint64_t d, uint64_t heads,
                                uint64_t T, uint64_t B, uint32_t box_tokens);
+
+// Encode a 4-D bf16 tensor map over a paged cache (element (page, slot, head, j) at page *
+// page_stride + slot * slot_stride + head * head_stride + j) with a box of `box_slots` slots (a
+// multiple of 8) of one head and 64 columns, 128-byte swizzle: [box_slots][64] of the canonical layout.
+// A page outside 0 .. pages - 1 reads as zero. Strides below 2^40 bytes.
+cudaError_t encode_tmap_paged(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads, uint64_t slots,
+                              uint64_t pages, uint64_t head_stride, uint64_t slot_stride, uint64_t page_stride,
+                              uint32_t box_slots);
 
 }  // namespace tc
 }  // namespace gdn

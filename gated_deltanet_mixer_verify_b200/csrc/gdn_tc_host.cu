@@ -59,5 +59,24 @@ cudaError_t encode_tmap_tokens(CUtensorMap* map, const void* base, bool bf16, ui
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_tmap_paged(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads, uint64_t slots,
+                              uint64_t pages, uint64_t head_stride, uint64_t slot_stride, uint64_t page_stride,
+                              uint32_t box_slots) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    cudaError_t e = encoder(&encode);
+    if (e != cudaSuccess) return e;
+    if (d % 64 != 0 || box_slots % 8 != 0 || box_slots == 0 || box_slots > 256) return cudaErrorInvalidValue;
+    // an axis with one entry has no stride of its own: any valid one will do
+    const cuuint64_t dims[4] = {d, heads, slots, pages};
+    const cuuint64_t strides[3] = {2 * (heads == 1 ? d : head_stride), 2 * (slots == 1 ? d : slot_stride),
+                                   2 * (pages == 1 ? d : page_stride)};
+    const cuuint32_t box[4] = {64, 1, box_slots, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace tc
 }  // namespace gdn
