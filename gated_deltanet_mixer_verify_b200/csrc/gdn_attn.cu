@@ -37,6 +37,7 @@ struct Geo {
     static constexpr int kStages = kStage <= 4096 ? 4 : kStage <= 16384 ? 3 : 2;
     static constexpr int kCtasPerSm = kStage <= 4096 ? 3 : kStage <= 8192 ? 2 : 1;
     static constexpr int kUnit = 16 * kWarps;                    // positions per unit
+    static constexpr int kExtra = 3;                             // units that an item costs besides
     static constexpr int kMaxTiles = D <= 128 ? 2 : 1;           // 16-row tiles a warp's registers hold
     static constexpr int kRing = kStages * kStage;               // bytes per warp
 };
@@ -273,7 +274,9 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
     const int C = gridDim.x, c = blockIdx.x, tile = blockIdx.y;
     // the join kernel may take its place on the SMs now; it waits for this one to end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Start at = find_start<NT>(x, s_start, c, C, c == 0 && tile == 0);
+    int kv0, rows0;
+    ask_counts(a, kv0, rows0);
+    const Start at = find_start<NT, G::kUnit, G::kExtra>(x, s_start, c, C, tile, kv0, rows0);
 
     unsigned char* ring = smem + warp * G::kRing;
     unsigned char* q_tile = smem + NW * G::kRing;
@@ -283,7 +286,7 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
     const E* kc = static_cast<const E*>(a.cache.k);
     const E* vc = static_cast<const E*>(a.cache.v);
 
-    Walk w(at);
+    Walk<G::kUnit, G::kExtra> w(at);
     while (w.next(x)) {
         if (row0 / share >= w.s.rows) continue;                                // none of this tile's rows
         const Seq& s = w.s;
@@ -500,6 +503,7 @@ Plan plan_stream(int sms, int rows) {
     while (mt < G::kMaxTiles && 16 * mt < rows) mt *= 2;
     Plan p;
     p.unit = G::kUnit;
+    p.extra = G::kExtra;
     p.rows = 16 * mt;
     p.tiles = (rows + p.rows - 1) / p.rows;
     p.ctas = std::max(1, sms * G::kCtasPerSm / p.tiles);
@@ -540,8 +544,8 @@ size_t paged_attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, bool
     using namespace attn;
     if (B == 0) return 0;
     const int rows = Hq / Hk * T;
-    size_t n = parts_bytes(plan_of(kMaxSms, rows, d, bf16), B, d);
-    if (bf16) n = std::max(n, parts_bytes(plan_tc(kMaxSms, rows), B, d));
+    size_t n = parts_bytes(plan_of(kMaxSms, rows, d, bf16), d);
+    if (bf16) n = std::max(n, parts_bytes(plan_tc(kMaxSms, rows), d));
     return n;
 }
 
@@ -556,9 +560,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
     const Plan p = on_tc ? plan_tc(sms, rows) : plan_of(sms, rows, a.d, a.bf16);
     Args x;
     x.a = a;
-    x.parts = parts_at(a.workspace, p, a.B, a.d);
+    x.parts = parts_at(a.workspace, p, a.d);
     x.rows = p.rows;
-    x.unit = p.unit;
     x.c = a.scale * kLog2e;
     if (on_tc) return launch_tc(x, p, stream);
     if (a.bf16)

@@ -2,12 +2,12 @@
 // the streaming kernel, the tensor-memory kernel and the join kernel. Not part of the public
 // interface.
 //
-// The lengths are on the device, so the split is made there. Every sequence b contributes n_b units
-// of `unit` positions (from the first position that any of its rows sees) for each key head; the
-// units of a launch, ordered by sequence, key head and position, are dealt evenly to C CTAs, CTA c
-// taking units floor(W c / C) .. floor(W (c + 1) / C). A CTA therefore walks whole (sequence, head)
-// items, and at most its first and its last one only in part. Parts go to the workspace (two slots
-// per CTA) and the join kernel adds them up in the order of the CTAs, so the result does not depend
+// The lengths are on the device, so the split is made there. Every sequence b contributes, for each
+// key head, an item of n_b units of `unit` positions (from the first position that any of its rows
+// sees) and `extra` more that stand for the cost of an item itself. The units of a launch, ordered by
+// sequence, key head and position, are dealt evenly to C CTAs, each a run of them. A CTA therefore walks whole (sequence,
+// head) items, and at most its first and its last one only in part. Parts go to the workspace (two
+// slots per CTA) and the join kernel adds them up in the order of the CTAs, so the result does not depend
 // on timing, however the lengths are spread.
 #pragma once
 
@@ -28,27 +28,37 @@ constexpr float kLn2 = 0.6931471805599453f;
 // How one launch is laid out (host).
 struct Plan {
     int unit;       // positions per unit
+    int extra;      // units that an item costs besides its positions
     int rows;       // rows per row tile (blockIdx.y): row r = t (H_q / H_kv) + head within the group
     int tiles;      // row tiles
     int ctas;       // CTAs per row tile (C)
     int slots() const { return ctas > 1 ? ctas * tiles * 2 : 0; }
 };
 
-// The workspace: the units of the sequences before b (int64 [B + 1]), then per (row tile, CTA, slot)
-// rows x D sums, and rows maxima and rows totals.
+// An item that was split: its sequence and key head, its first and last CTA, and the first one's slot.
+// CTA c writes the entry of its own beginning: b = -1 unless it begins inside an item, and is the
+// second CTA to work on it.
+struct __align__(16) Lead {
+    int b, h, c0, c1_slot;
+};
+
+// The workspace: the number of units and the leads, then per (row tile, CTA, slot) rows x D sums, and rows
+// maxima and rows totals.
 struct Parts {
-    int64_t* before;
-    float* o;       // [tiles][C][2][rows][D]
-    float* m;       // [tiles][C][2][rows], base-2 exponents
+    int64_t* units;   // [2], the second unused
+    Lead* lead;       // [C]
+    float* o;         // [tiles][C][2][rows][D]
+    float* m;         // [tiles][C][2][rows], base-2 exponents
     float* l;
 };
-inline size_t parts_bytes(const Plan& p, int B, int D) {
-    return (((size_t)B + 1) * 8 + 15) / 16 * 16 + (size_t)p.slots() * p.rows * ((size_t)D + 2) * 4;
+inline size_t parts_bytes(const Plan& p, int D) {
+    return p.ctas < 2 ? 0 : 16 + (size_t)p.ctas * sizeof(Lead) + (size_t)p.slots() * p.rows * ((size_t)D + 2) * 4;
 }
-inline Parts parts_at(void* ws, const Plan& p, int B, int D) {
+inline Parts parts_at(void* ws, const Plan& p, int D) {
     Parts r;
-    r.before = static_cast<int64_t*>(ws);
-    r.o = reinterpret_cast<float*>(static_cast<char*>(ws) + (((size_t)B + 1) * 8 + 15) / 16 * 16);
+    r.units = static_cast<int64_t*>(ws);
+    r.lead = reinterpret_cast<Lead*>(static_cast<char*>(ws) + 16);
+    r.o = reinterpret_cast<float*>(r.lead + p.ctas);
     r.m = r.o + (size_t)p.slots() * p.rows * D;
     r.l = r.m + (size_t)p.slots() * p.rows;
     return r;
@@ -58,7 +68,7 @@ inline Parts parts_at(void* ws, const Plan& p, int B, int D) {
 struct Args {
     AttnArgs a;
     Parts parts;
-    int rows, unit;
+    int rows;
     float c;        // scale log2(e): the softmax runs on base-2 exponents
 };
 
@@ -66,45 +76,61 @@ struct Args {
 struct Seq {
     int kv, rows;   // positions, rows of the block
     int first;      // first position that any row sees
-    int units;
+    int units;      // of an item, and with its extra ones
+    int span;
 };
-__device__ __forceinline__ Seq read_seq(const AttnArgs& a, int unit, int b, bool& bad) {
+template <int UNIT, int EXTRA>
+__device__ __forceinline__ Seq make_seq(const AttnArgs& a, int kv, int rows, bool& bad) {
     Seq s;
-    s.kv = a.kv_len[b];
-    s.rows = a.q_len ? a.q_len[b] : a.T;
-    bad = s.kv < 0 || s.kv > a.max_pages * a.cache.page || s.rows < 0 || s.rows > a.T;
+    s.kv = kv;
+    s.rows = rows;
+    bad = kv < 0 || kv > a.max_pages * a.cache.page || rows < 0 || rows > a.T;
     if (bad) s.kv = s.rows = 0;
     const int p0 = s.kv - s.rows;
-    s.first = a.window > 0 ? max(0, p0 - a.window + 1) / unit * unit : 0;
-    s.units = s.rows == 0 ? 0 : max(1, (s.kv - s.first + unit - 1) / unit);   // a row that sees nothing is written too
+    s.first = a.window > 0 ? max(0, p0 - a.window + 1) / UNIT * UNIT : 0;
+    s.units = s.rows == 0 ? 0 : max(1, (s.kv - s.first + UNIT - 1) / UNIT);   // a row that sees nothing is written too
+    s.span = s.rows == 0 ? 0 : s.units + EXTRA;
     return s;
 }
+template <int UNIT, int EXTRA>
+__device__ __forceinline__ Seq read_seq(const AttnArgs& a, int b, bool& bad) {
+    const int kv = a.kv_len[b], rows = a.q_len ? a.q_len[b] : a.T;
+    return make_seq<UNIT, EXTRA>(a, kv, rows, bad);
+}
 
-// First unit of CTA c of C.
-__device__ __forceinline__ int64_t first_unit(int64_t W, int c, int C) { return W * c / C; }
-// The CTA that takes unit u.
-__device__ __forceinline__ int cta_of(int64_t W, int64_t u, int C) { return (int)(((u + 1) * C + W - 1) / W) - 1; }
+// W units dealt to C CTAs: the first W % C get one more than the others.
+struct Deal {
+    int64_t each, more;
+    __device__ __forceinline__ Deal(int64_t W, int C) : each(W / C), more(W - each * C) {}
+    __device__ __forceinline__ int64_t first(int c) const { return c * each + min((int64_t)c, more); }
+    __device__ __forceinline__ int cta_of(int64_t u) const {
+        const int64_t t = more * (each + 1);
+        return (int)(u < t ? u / (each + 1) : more + (u - t) / each);
+    }
+};
 
 // Where a CTA begins: its units [u, end), and the sequence that unit u falls into, whose units
-// begin at `base`. All NT threads call it; sm holds NT / 32 + 2 entries. CTA (0, 0) also leaves the
-// sequences' first units for the join.
+// begin at `base`. All NT threads call it, with the counts of sequence threadIdx.x already asked for
+// (0 rows where there is none), so that what the caller does in between hides their latency; sm holds
+// NT / 32 + 2 entries. CTAs of row tile 0 leave the leads for the join.
 struct Start {
     int64_t u, end, base;
     int b;
 };
-template <int NT>
-__device__ __forceinline__ Start find_start(const Args& x, int64_t* sm, int c, int C, bool write) {
+template <int NT, int UNIT, int EXTRA>
+__device__ __forceinline__ Start find_start(const Args& x, int64_t* sm, int c, int C, int tile, int kv0, int rows0) {
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // NT sequences or fewer: one for each thread. More: a run of them for each.
     const int per = (a.B + NT - 1) / NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int64_t mine = 0;
     bool any_bad = false;
     for (int b = b0; b < b1; ++b) {
         bool bad;
-        mine += (int64_t)read_seq(a, x.unit, b, bad).units * a.Hk;
+        mine += (int64_t)(per == 1 ? make_seq<UNIT, EXTRA>(a, kv0, rows0, bad) : read_seq<UNIT, EXTRA>(a, b, bad)).span * a.Hk;
         any_bad |= bad;
     }
-    if (write && any_bad && a.status_word) atomicOr(a.status_word, dev::kStatusBadLength);
+    if (c == 0 && tile == 0 && any_bad && a.status_word) atomicOr(a.status_word, dev::kStatusBadLength);
     int64_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -119,39 +145,58 @@ __device__ __forceinline__ Start find_start(const Args& x, int64_t* sm, int c, i
         if (w < warp) before += sm[w];
         W += sm[w];
     }
-    if (write) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            bool bad;
-            x.parts.before[b] = at;
-            at += (int64_t)read_seq(a, x.unit, b, bad).units * a.Hk;
-        }
-        if (tid == 0) x.parts.before[a.B] = W;
-    }
+    const Deal deal(W, C);
     Start s;
-    s.u = first_unit(W, c, C);
-    s.end = first_unit(W, c + 1, C);
+    s.u = deal.first(c);
+    s.end = deal.first(c + 1);
     if (s.u < s.end && before <= s.u && s.u < before + mine) {
         int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            bool bad;
-            const int64_t n = (int64_t)read_seq(a, x.unit, b, bad).units * a.Hk;
-            if (s.u < at + n) {
-                sm[NT / 32] = b;
-                sm[NT / 32 + 1] = at;
-                break;
-            }
-            at += n;
+        int b = b0;
+        bool bad;
+        Seq q = read_seq<UNIT, EXTRA>(a, b, bad);
+        while (s.u >= at + (int64_t)q.span * a.Hk) {
+            at += (int64_t)q.span * a.Hk;
+            q = read_seq<UNIT, EXTRA>(a, ++b, bad);
         }
+        sm[NT / 32] = b;
+        sm[NT / 32 + 1] = at;
+        if (C > 1 && tile == 0) {
+            Lead lead = {-1, 0, 0, 0};
+            const int h = (int)((s.u - at) / q.span);
+            const int64_t u0 = at + (int64_t)h * q.span;
+            if (s.u > u0 && s.u < u0 + q.units) {
+                const int c0 = deal.cta_of(u0);
+                if (deal.cta_of(s.u - 1) == c0) {
+                    lead.b = b;
+                    lead.h = h;
+                    lead.c0 = c0;
+                    lead.c1_slot = deal.cta_of(u0 + q.units - 1) * 2 + (deal.first(c0) == u0 ? 0 : 1);
+                }
+            }
+            x.parts.lead[c] = lead;
+        }
+    }
+    if (C > 1 && tile == 0 && tid == 0) {
+        if (s.u >= s.end) x.parts.lead[c] = Lead{-1, 0, 0, 0};
+        if (c == 0) x.parts.units[0] = W;
     }
     __syncthreads();
     s.b = (int)sm[NT / 32];
     s.base = sm[NT / 32 + 1];
     return s;
 }
+// The counts of sequence threadIdx.x, for find_start.
+__device__ __forceinline__ void ask_counts(const AttnArgs& a, int& kv, int& rows) {
+    kv = rows = 0;
+    if ((int)threadIdx.x < a.B) {
+        kv = a.kv_len[threadIdx.x];
+        rows = a.q_len ? a.q_len[threadIdx.x] : a.T;
+    }
+}
 
 // A CTA's walk over its items: next() moves to the next (sequence, key head) and the part of its units
 // that is this CTA's. Every thread of the CTA walks alike.
+template <int UNIT, int EXTRA>
 struct Walk {
     int64_t u, begin, end, base;
     int b, h, i0, i1;      // sequence, key head, units i0 .. i1 of the item
@@ -160,20 +205,24 @@ struct Walk {
     int slot;              // where a part goes
     __device__ __forceinline__ Walk(const Start& at) : u(at.u), begin(at.u), end(at.end), base(at.base), b(at.b) {}
     __device__ __forceinline__ bool next(const Args& x) {
-        if (u >= end) return false;
-        bool bad;
-        s = read_seq(x.a, x.unit, b, bad);
-        while (u >= base + (int64_t)s.units * x.a.Hk) {
-            base += (int64_t)s.units * x.a.Hk;
-            s = read_seq(x.a, x.unit, ++b, bad);
+        while (u < end) {
+            bool bad;
+            s = read_seq<UNIT, EXTRA>(x.a, b, bad);
+            while (u >= base + (int64_t)s.span * x.a.Hk) {
+                base += (int64_t)s.span * x.a.Hk;
+                s = read_seq<UNIT, EXTRA>(x.a, ++b, bad);
+            }
+            const int64_t in = u - base;
+            h = in >> 31 ? (int)(in / s.span) : (int)((uint32_t)in / (uint32_t)s.span);
+            i0 = (int)(in - (int64_t)h * s.span);
+            const int stop = (int)min((int64_t)s.span, end - u + i0);
+            i1 = min(stop, s.units);
+            whole = i0 == 0 && i1 == s.units;
+            slot = u == begin ? 0 : 1;
+            u += stop - i0;
+            if (i0 < i1) return true;      // else only extra units were left of it
         }
-        h = (int)((u - base) / s.units);
-        i0 = (int)(u - base - (int64_t)h * s.units);
-        i1 = (int)min((int64_t)s.units, end - u + i0);
-        whole = i0 == 0 && i1 == s.units;
-        slot = u == begin ? 0 : 1;
-        u += i1 - i0;
-        return true;
+        return false;
     }
 };
 

@@ -3,9 +3,10 @@
 //
 // With m_i, l_i, o_i the maxima, totals and sums of the parts i of a row, in base 2:
 //   m = max m_i,  l = sum 2^(m_i - m) l_i,  o = sum 2^(m_i - m) o_i / l,  lse = (m + log2 l) ln 2.
-// One CTA per (border between two CTAs' units, row): the CTA of an item's first border does the
-// row, all others return, so items that were not split cost nothing. Four warps take the parts
-// in turn. Launched as a programmatic dependent: its CTAs are in place when the last part is written.
+// A small grid, launched as a programmatic dependent so that it is in place when the last part is
+// written. Every CTA gathers the split items from the leads that the kernel before left, and takes rows in
+// turn: a warp for each row, eight parts in flight, or all its warps for one row where there are few
+// rows (then each has many parts). Bound by the latency of two dependent reads.
 #include "gdn_attn.cuh"
 
 namespace gdn {
@@ -14,121 +15,151 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxLeads = kMaxSms * 3;      // CTAs per row tile at most
 
+// A row's running sums.
+template <int N>
+struct Sum {
+    float m, l, o[N];
+};
+
+// Parts p0, p0 + step, ... below end of one row.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) gdn_paged_attention_join_kernel(const __grid_constant__ Args x, int C) {
-    constexpr int N = D / 32;
-    __shared__ float s_o[kWarps][D], s_m[kWarps], s_l[kWarps];
-    const AttnArgs& a = x.a;
-    const int c = blockIdx.x + 1, G = a.Hq / a.Hk;
-    const int tile = blockIdx.y / x.rows, r = blockIdx.y % x.rows, row = tile * x.rows + r;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (row >= G * a.T) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t W = x.parts.before[a.B];
-    const int64_t u = first_unit(W, c, C);
-    if (u == 0 || u >= W) return;
-    // the sequence of unit u - 1 and of unit u: the last b with before[b] <= u that has units
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (x.parts.before[mid] <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    const int b = lo;
-    const int64_t base = x.parts.before[b];
-    const int n = (int)((x.parts.before[b + 1] - base) / a.Hk);
-    const int h = (int)((u - base) / n);
-    const int64_t u0 = base + (int64_t)h * n, u1 = u0 + n;
-    if (u == u0) return;                                   // a border between items
-    const int c0 = cta_of(W, u0, C), c1 = cta_of(W, u1 - 1, C);
-    if (c != c0 + 1) return;
-    const int t = row / G, q_rows = a.q_len ? a.q_len[b] : a.T;
-    if (t >= q_rows) return;
-
-    const int first_slot = first_unit(W, c0, C) == u0 ? 0 : 1;
-    float m = -INFINITY, l = 0.f, o[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = 0.f;
-    // eight parts in flight for each warp
-    constexpr int F = 8;
-    for (int p = c0 + warp; p <= c1; p += kWarps * F) {
+__device__ __forceinline__ void add_parts(const Args& x, const Deal& deal, int C, int tile, int r, const Lead& it, int p0, int step,
+                                          int lane, Sum<D / 32>& s) {
+    constexpr int N = D / 32, F = 8;
+    const int c1 = it.c1_slot >> 1;
+    for (int p = p0; p <= c1; p += step * F) {
         float pm[F], pl[F], po[F][N];
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            const int cc = p + f * kWarps;
+            const int cc = p + f * step;
             pm[f] = -INFINITY;
             pl[f] = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) po[f][i] = 0.f;
             // with fewer units than CTAs some have none, and left nothing
-            if (cc <= c1 && first_unit(W, cc, C) < first_unit(W, cc + 1, C)) {
-                const size_t at = (((size_t)tile * C + cc) * 2 + (cc == c0 ? first_slot : 0)) * x.rows + r;
+            if (cc <= c1 && deal.first(cc) < deal.first(cc + 1)) {
+                const size_t at = (((size_t)tile * C + cc) * 2 + (cc == it.c0 ? (it.c1_slot & 1) : 0)) * x.rows + r;
                 pm[f] = x.parts.m[at];
                 pl[f] = x.parts.l[at];
 #pragma unroll
                 for (int i = 0; i < N; ++i) po[f][i] = x.parts.o[at * D + i * 32 + lane];
             }
         }
-        float top = m;
+        float top = s.m;
 #pragma unroll
         for (int f = 0; f < F; ++f) top = fmaxf(top, pm[f]);
         const float use = top == -INFINITY ? 0.f : top;
-        const float k = exp2_approx(m - use);
-        l *= k;
+        const float k = exp2_approx(s.m - use);
+        s.l *= k;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] *= k;
+        for (int i = 0; i < N; ++i) s.o[i] *= k;
 #pragma unroll
         for (int f = 0; f < F; ++f) {
             const float w = exp2_approx(pm[f] - use);
-            l = fmaf(w, pl[f], l);
+            s.l = fmaf(w, pl[f], s.l);
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = fmaf(w, po[f][i], o[i]);
+            for (int i = 0; i < N; ++i) s.o[i] = fmaf(w, po[f][i], s.o[i]);
         }
-        m = top;
+        s.m = top;
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(const __grid_constant__ Args x, int C, int all_rows) {
+    constexpr int N = D / 32;
+    __shared__ Lead s_lead[kMaxLeads];
+    __shared__ int s_count[kWarps];
+    __shared__ float s_o[kWarps][D], s_m[kWarps], s_l[kWarps];
+    const AttnArgs& a = x.a;
+    const int G = a.Hq / a.Hk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t W = x.parts.units[0];
+    // the split items, in the order of their leads
+    int n = 0;
+    for (int base = 1; base < C; base += kThreads) {
+        const int c = base + threadIdx.x;
+        Lead it = {-1, 0, 0, 0};
+        if (c < C) it = x.parts.lead[c];
+        const unsigned ballot = __ballot_sync(kFull, it.b >= 0);
+        if (lane == 0) s_count[warp] = __popc(ballot);
+        __syncthreads();
+        int at = n + __popc(ballot & ((1u << lane) - 1));
 #pragma unroll
-    for (int i = 0; i < N; ++i) s_o[warp][i * 32 + lane] = o[i];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += s_count[w];
+            n += s_count[w];
+        }
+        if (it.b >= 0) s_lead[at] = it;
+        __syncthreads();
     }
-    __syncthreads();
-    float top = -INFINITY;
+    if (n == 0) return;
+    const Deal deal(W, C);
+    const int64_t tasks = (int64_t)n * all_rows;
+    const bool together = tasks <= gridDim.x;     // a CTA for each row
+    for (int64_t i = together ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp; i < tasks; i += (int64_t)gridDim.x * (together ? 1 : kWarps)) {
+        const int k = (int)(i / all_rows), row = (int)(i - (int64_t)k * all_rows);
+        const Lead it = s_lead[k];
+        const int tile = row / x.rows, r = row - tile * x.rows, t = row / G;
+        if (t >= (a.q_len ? a.q_len[it.b] : a.T)) continue;
+        Sum<N> s;
+        s.m = -INFINITY;
+        s.l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float use = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, k[kWarps];
+        for (int e = 0; e < N; ++e) s.o[e] = 0.f;
+        add_parts<D>(x, deal, C, tile, r, it, it.c0 + (together ? warp : 0), together ? kWarps : 1, lane, s);
+        const int64_t out = ((int64_t)it.b * a.T + t) * a.Hq + (int64_t)it.h * G + (row - t * G);
+        if (!together) {
+            const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        k[w] = exp2_approx(s_m[w] - use);
-        sum += k[w] * s_l[w];
+            for (int e = 0; e < N; ++e) store_o(a, out * D + e * 32 + lane, s.o[e] * inv);
+            if (lane == 0 && a.lse) a.lse[out] = ((s.m == -INFINITY ? 0.f : s.m) + log2f(s.l)) * kLn2;
+            continue;
+        }
+        // one row for each CTA: no second round, so s_o is written once
+#pragma unroll
+        for (int e = 0; e < N; ++e) s_o[warp][e * 32 + lane] = s.o[e];
+        if (lane == 0) {
+            s_m[warp] = s.m;
+            s_l[warp] = s.l;
+        }
+        __syncthreads();
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
+        const float use = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, f[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            f[w] = exp2_approx(s_m[w] - use);
+            sum = fmaf(f[w], s_l[w], sum);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int e = threadIdx.x; e < D; e += kThreads) {
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) y = fmaf(f[w], s_o[w][e], y);
+            store_o(a, out * D + e, y * inv);
+        }
+        if (threadIdx.x == 0 && a.lse) a.lse[out] = (use + log2f(sum)) * kLn2;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t out = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * G + (row - t * G);
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-        float y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) y = fmaf(k[w], s_o[w][i], y);
-        store_o(a, out * D + i, y * inv);
-    }
-    if (threadIdx.x == 0 && a.lse) a.lse[out] = (use + log2f(sum)) * kLn2;
 }
 
 template <int D>
 cudaError_t launch(const Args& x, const Plan& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    const int rows = x.a.Hq / x.a.Hk * x.a.T;
-    cfg.gridDim = dim3(p.ctas - 1, (rows + p.rows - 1) / p.rows * p.rows);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.gridDim = dim3(2 * kMaxSms);
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_paged_attention_join_kernel<D>, x, p.ctas);
+    return cudaLaunchKernelEx(&cfg, gdn_paged_attention_join_kernel<D>, x, p.ctas, x.a.Hq / x.a.Hk * x.a.T);
 }
 
 }  // namespace

@@ -44,6 +44,7 @@ namespace {
 using namespace dev;
 
 constexpr int kTile = 128;                      // positions per tile, and per unit
+constexpr int kExtra = 2;                       // units that an item costs besides (its first and last steps overlap nothing)
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
@@ -180,10 +181,14 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     // the join kernel may take its place on the SMs now; it waits for this one to end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    int kv0, rows0;
+    ask_counts(a, kv0, rows0);
     const uint32_t raw = smem_u32(smem_raw), ring_at = (raw + 1023u) & ~1023u;
     unsigned char* const ring = smem_raw + (ring_at - raw);
     constexpr uint32_t kQOff = G::kSlots * kBlock, kPOff = kQOff + G::kQ;
     if (tid == 0) {
+        tc::prefetch_tmap(&k_map);
+        tc::prefetch_tmap(&v_map);
         for (int i = 0; i < G::kSlots; ++i) {
             mbar_init(&bars.kv_full[i], 1);
             mbar_init(&bars.kv_empty[i], 1);
@@ -208,7 +213,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     // rows of Q that are nobody's stay zero
     for (int i = tid; i < G::kQ / 16; i += G::kThreads) reinterpret_cast<uint4*>(ring + kQOff)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
-    const Start at = find_start<G::kThreads>(x, s_start, c, C, c == 0 && mtile == 0);
+    const Start at = find_start<G::kThreads, kTile, kExtra>(x, s_start, c, C, mtile, kv0, rows0);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -216,7 +221,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
 
     const int share = a.Hq / a.Hk, row0 = mtile * x.rows, all_rows = share * a.T;
     const int rows = min(x.rows, all_rows - row0);
-    Walk w(at);
+    Walk<kTile, kExtra> w(at);
 
     if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax and outputs
@@ -409,14 +414,19 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
-            // Lane i looks up the page of run i; num_pages (which TMA reads as zeros) where nothing of it is
-            // seen or its page is not in the pool.
-            auto look_up = [&](int j) -> int {
+            // Lane i looks up the page of run i of tile j, and makes it num_pages (which TMA reads as zeros)
+            // where nothing of the run is seen or the page is not in the pool.
+            auto needed = [&](int j) -> bool {
                 const int pos = first + j * kTile + lane * run;
-                if (lane >= runs || j >= n || pos >= w.s.kv || pos + run <= see.lo_min) return a.cache.num_pages;
-                const int id = a.table[(int64_t)w.b * a.max_pages + pos / page];
-                if ((unsigned)id < (unsigned)a.cache.num_pages) return id;
-                if (a.status_word) atomicOr(a.status_word, kStatusBadPage);
+                return lane < runs && j < n && pos < w.s.kv && pos + run > see.lo_min;
+            };
+            auto look_up = [&](int j) -> int {
+                return needed(j) ? a.table[(int64_t)w.b * a.max_pages + (first + j * kTile + lane * run) / page] : 0;
+            };
+            auto page_of = [&](int j, int id) -> int {
+                const bool need = needed(j);
+                if (need && (unsigned)id < (unsigned)a.cache.num_pages) return id;
+                if (need && a.status_word) atomicOr(a.status_word, kStatusBadPage);
                 return a.cache.num_pages;
             };
             auto fetch = [&](const CUtensorMap* map, int j, int id) -> bool {
@@ -433,9 +443,10 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 return true;
             };
             // K 0, K 1, V 0, K 2, V 1, ...; pages are looked up a tile ahead of their use
-            int id_v = a.cache.num_pages, id_k = look_up(0), id_next = look_up(1);
+            int id_v = 0, id_k = look_up(0), id_next = look_up(1);
             for (int j = 0; j <= n; ++j) {
                 if (j < n) {
+                    id_k = page_of(j, id_k);
                     // the tile's positions that are there, 32 to a word
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -640,6 +651,7 @@ bool tc_applies(const AttnArgs& a) {
 Plan plan_tc(int sms, int rows) {
     Plan p;
     p.unit = kTile;
+    p.extra = kExtra;
     p.rows = std::min(rows, 128);
     p.tiles = (rows + 127) / 128;
     p.ctas = std::max(1, sms / p.tiles);

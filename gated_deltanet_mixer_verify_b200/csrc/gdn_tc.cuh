@@ -220,6 +220,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 
 // ---------------------------------------------------------------- tensor TMA
 
+// Brings a tensor map (a kernel parameter) near, ahead of its first use.
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // 2-D tiled tensor copy global -> shared, completion counted on `bar`. c0 is the inner
 // (contiguous) coordinate in elements; c0 * element size must be a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
