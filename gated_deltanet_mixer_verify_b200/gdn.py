@@ -12,6 +12,7 @@ the runtime paragraph) over a verify block of 7 drafts + 1 anchor ("Qwen 3.8 27B
 """
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -45,21 +46,6 @@ class _AcceptShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("logits_dtype", ctypes.c_int32), ("sampled", ctypes.c_int32),
                 ("temperature", ctypes.c_float)]
-
-
-class _KvShape(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32),
-                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
-                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("status_word", ctypes.c_void_p)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("rot", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
-                ("axes_interleaved", ctypes.c_int32), ("pairs_interleaved", ctypes.c_int32),
-                ("norm_eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
-                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -97,11 +83,11 @@ def _load():
     lib.gdn_verify_step_gated.argtypes = [S] + [_VP] * 12 + [ctypes.c_float] + [_VP] * 3
     lib.gdn_gated_rmsnorm.argtypes = [ctypes.c_int64, ctypes.c_int32, _VP, ctypes.c_int32, _VP, ctypes.c_int32,
                                       _VP, ctypes.c_float, _VP, ctypes.c_int32, _VP]
-    K = ctypes.POINTER(_KvShape)
-    lib.gdn_kv_plan.argtypes = [K] + [_VP] * 15
-    lib.gdn_rope_append.argtypes = [K, ctypes.POINTER(_Rope)] + [_VP] * 14
-    lib.gdn_paged_attention.argtypes = ([K, ctypes.c_float, ctypes.c_int32] + [_VP] * 9 + [ctypes.c_size_t, _VP])
-    lib.gdn_paged_attention_workspace_bytes.argtypes = [K]
+    # gdn_kv_shape and gdn_rope come packed, as bytes
+    lib.gdn_kv_plan.argtypes = [_VP] * 16
+    lib.gdn_rope_append.argtypes = [_VP] * 16
+    lib.gdn_paged_attention.argtypes = ([_VP, ctypes.c_float, ctypes.c_int32] + [_VP] * 9 + [ctypes.c_size_t, _VP])
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [_VP]
     lib.gdn_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     for fn in ("gdn_kv_plan", "gdn_rope_append", "gdn_paged_attention", "gdn_verify_step", "gdn_commit", "gdn_decode_step", "gdn_commit_and_verify", "gdn_chunk_prefill",
                "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_prepare", "gdn_chunk_prefill_scan",
@@ -495,98 +481,107 @@ def chunk_prefill_noalloc(q, k, v, a, b, A_log, dt_bias, state_in=None, state_ou
     return o, state_out
 
 
-def _one_type(dt, **ts):
-    for name, t in ts.items():
-        if t is not None and t.dtype != dt:
-            raise TypeError("%s must be %s, not %s" % (name, str(dt)[6:], t.dtype))
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+# gdn_kv_shape (B, T, H_q, H_kv, d, dtype, out_dtype, page_size, num_pages, max_pages; page, slot and
+# head strides; status_word) and gdn_rope (rot, n_axes, sections, axes_interleaved,
+# pairs_interleaved, norm_eps; q, k, v and q_out strides), laid out as the C structs are.
+_pack_kv_shape = struct.Struct("=10i3qQ").pack
+_pack_rope = struct.Struct("=8if4x4q").pack
 
 
-def _one_shape(shape, **ts):
-    for name, t in ts.items():
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError("%s must be %s, not %s" % (name, list(shape), list(t.shape)))
+def _want(name, t, dt, shape, dev):
+    """Device pointer of a contiguous tensor of one type and shape on device ``dev``; None stays None.
+    (Straight-line checks: these calls take up to fourteen tensors, and small ones are over in
+    a few microseconds.)"""
+    if t is None:
+        return None
+    if t.dtype is not dt:
+        raise TypeError("%s must be %s, not %s" % (name, str(dt)[6:], t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, not %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not where the other tensors are" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous tensor" % name)
+    return t.data_ptr()
 
 
-def _strided_ptrs(*ts):
-    """Device pointers of tensors whose strides the call takes: on the current device, their last
-    axis contiguous (what the other strides may be is the caller's to check)."""
-    cur = torch.cuda.current_device() if ts[0].is_cuda else None
-    out = []
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if t.get_device() != cur:
-            raise ValueError("tensor is on cuda:%d but the current CUDA device is cuda:%d; call under "
-                             "torch.cuda.device(%d)" % (t.get_device(), cur, t.get_device()))
-        if t.stride(-1) != 1:
-            raise ValueError("expected a contiguous last axis")
-        out.append(t.data_ptr())
-    return out
+def _raw_stream(stream, dev) -> int:
+    """The stream to launch on, after the last check of the tensors' common device."""
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError("tensor is on cuda:%d but the current CUDA device is cuda:%d; call under "
+                         "torch.cuda.device(%d)" % (dev, cur, dev))
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _token_stride(name, t) -> int:
+def _token_stride(name, t, B, T, H, d) -> int:
     """Elements between the tokens of t [B, T, heads, d] (its heads contiguous within a token, its
     sequences T tokens apart): a slice of a projection's output, or a contiguous tensor."""
-    B, T, H, d = t.shape
-    sb, st, sh, _ = t.stride()
+    sb, st, sh, sd = t.stride()
     if T == 1:
         st = sb if B > 1 else H * d
-    if (H > 1 and sh != d) or (B > 1 and sb != T * st):
+    if sd != 1 or (H > 1 and sh != d) or (B > 1 and sb != T * st):
         raise ValueError("%s must be [B, T, heads, d] with one stride from token to token and contiguous heads" % name)
     return st
 
 
-def _kv_shape(B, T, H_q, H_kv, d, dtype, out_dtype, page_size, num_pages, max_pages, strides, status_word) -> _KvShape:
-    if status_word is not None:
-        _one_type(torch.int32, status_word=status_word)
-    return _KvShape(B, T, H_q, H_kv, d, dtype, out_dtype, page_size, num_pages, max_pages, *strides,
-                    _ptr(status_word))
-
-
-def _cache_strides(k_cache, v_cache, H_kv, d, dtype):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (H_kv, d):
+def _cache(k_cache, v_cache, H_kv, d, dtype, dev):
+    """(page size, pages, strides) of the caches."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or shape[2] != H_kv or shape[3] != d:
         raise ValueError("k_cache and v_cache must be [pages, page_size, %d, %d]" % (H_kv, d))
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("the caches must have the dtype of q (%s)" % dtype)
     strides = k_cache.stride()
     if strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same strides")
-    return strides[:3]
+    if strides[3] != 1:
+        raise ValueError("the caches' last axis must be contiguous")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError("the caches are not where q is")
+    return shape[1], shape[0], strides
 
 
 def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, commit_len=None, add_len=None,
             block_len=None, seq_len_out=None, n_pages_out=None, free_count_out=None, kv_len=None, q_len=None, slot_map=None,
             status_word=None, stream=None):
     """Block tables and slot maps of the next block, on the GPU: ``commit_len`` [B] of the last
-    block's tokens are kept (``block_len`` [B], the last call's q_len: at most that many), ``add_len`` [B] new ones (None: T each; -1: the request has ended) get
-    their pages and slots. seq_len, n_pages [B], block_table [B, max_pages], free_list [pages] and
-    free_count [1] are int32 and updated in place unless the ``_out`` arrays are given. Returns
-    (kv_len [B] int32, q_len [B] int32, slot_map [B, T] int64)."""
-    B, max_pages = block_table.shape
-    dev = block_table.device
-    seq_len_out = seq_len if seq_len_out is None else seq_len_out
-    n_pages_out = n_pages if n_pages_out is None else n_pages_out
-    free_count_out = free_count if free_count_out is None else free_count_out
+    block's tokens are kept (``block_len`` [B], the last call's q_len: at most that many), ``add_len``
+    [B] new ones (None: T each; -1: the request has ended) get their pages and slots. seq_len,
+    n_pages [B], block_table [B, max_pages], free_list [pages] and free_count [1] are int32 and
+    updated in place unless the ``_out`` arrays are given. Returns (kv_len [B] int32, q_len [B]
+    int32, slot_map [B, T] int64)."""
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_list [pages]")
+    B, max_pages = table_shape = block_table.shape
+    pages = free_list.shape
+    dev = block_table.get_device()
     if kv_len is None:
-        kv_len = torch.empty(B, dtype=torch.int32, device=dev)
+        kv_len = torch.empty(B, dtype=_I32, device=block_table.device)
     if q_len is None:
-        q_len = torch.empty(B, dtype=torch.int32, device=dev)
+        q_len = torch.empty(B, dtype=_I32, device=block_table.device)
     if slot_map is None:
-        slot_map = torch.empty((B, T), dtype=torch.int64, device=dev)
-    per_seq = dict(seq_len=seq_len, seq_len_out=seq_len_out, n_pages=n_pages, n_pages_out=n_pages_out, commit_len=commit_len,
-                   add_len=add_len, block_len=block_len, kv_len=kv_len, q_len=q_len)
-    _one_type(torch.int32, block_table=block_table, free_list=free_list, free_count=free_count,
-              free_count_out=free_count_out, **per_seq)
-    _one_type(torch.int64, slot_map=slot_map)
-    _one_shape((B,), **per_seq)
-    _one_shape((1,), free_count=free_count, free_count_out=free_count_out)
-    _one_shape((B, T), slot_map=slot_map)
-    if free_list.dim() != 1:
-        raise ValueError("free_list must be [pages]")
-    sh = _kv_shape(B, T, 1, 1, 64, GDN_BF16, GDN_BF16, page_size, free_list.shape[0], max_pages, (0, 0, 0), status_word)
-    _check(_load().gdn_kv_plan(ctypes.byref(sh), *_ptrs(seq_len, seq_len_out, commit_len, block_len, add_len, n_pages, n_pages_out,
-                                                       block_table, free_list, free_count, free_count_out, kv_len,
-                                                       q_len, slot_map), _stream(stream)))
+        slot_map = torch.empty((B, T), dtype=_I64, device=block_table.device)
+    per, one = (B,), (1,)
+    p_seq = _want("seq_len", seq_len, _I32, per, dev)
+    p_held = _want("n_pages", n_pages, _I32, per, dev)
+    p_count = _want("free_count", free_count, _I32, one, dev)
+    args = (p_seq, p_seq if seq_len_out is None else _want("seq_len_out", seq_len_out, _I32, per, dev),
+            _want("commit_len", commit_len, _I32, per, dev), _want("block_len", block_len, _I32, per, dev),
+            _want("add_len", add_len, _I32, per, dev),
+            p_held, p_held if n_pages_out is None else _want("n_pages_out", n_pages_out, _I32, per, dev),
+            _want("block_table", block_table, _I32, table_shape, dev), _want("free_list", free_list, _I32, pages, dev),
+            p_count, p_count if free_count_out is None else _want("free_count_out", free_count_out, _I32, one, dev),
+            _want("kv_len", kv_len, _I32, per, dev), _want("q_len", q_len, _I32, per, dev),
+            _want("slot_map", slot_map, _I64, (B, T), dev))
+    status = _want("status_word", status_word, _I32, one, dev) or 0
+    shape = _pack_kv_shape(B, T, 1, 1, 64, GDN_BF16, GDN_BF16, page_size, pages[0], max_pages, 0, 0, 0, status)
+    rc = _load().gdn_kv_plan(shape, *args, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return kv_len, q_len, slot_map
 
 
@@ -599,51 +594,51 @@ def rope_append(q, k, v, inv_freq, k_cache, v_cache, slot_map, positions=None, k
     (None: kv_len - q_len + t, both [B]) times inv_freq [rot / 2] fp32, and k, v go to ``slot_map``
     [B, T] int64 (-1: none) of the caches [pages, page_size, H_kv, d]. ``sections``: rotated pairs of
     each axis (None: one axis). Returns q_out (may be q)."""
-    B, T, H_q, d = q.shape
+    B, T, H_q, d = q_shape = q.shape
     H_kv = k.shape[2]
-    if tuple(k.shape) != (B, T, H_kv, d) or v.shape != k.shape:
+    if k.shape != (B, T, H_kv, d) or v.shape != k.shape:
         raise ValueError("q [B,T,H_q,d] and k, v [B,T,H_kv,d] disagree")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype, dev = q.dtype, q.get_device()
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise TypeError("q, k, v must share a dtype")
-    strides = _cache_strides(k_cache, v_cache, H_kv, d, q.dtype)
-    rot = 2 * inv_freq.shape[0]
-    sections = [rot // 2] if sections is None else list(sections)
-    if not 1 <= len(sections) <= 4:
+    page, pages, st = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
+    half = inv_freq.numel()
+    n_axes = 1 if sections is None else len(sections)
+    if not 1 <= n_axes <= 4:
         raise ValueError("one to four sections")
+    sec = (half, 0, 0, 0) if sections is None else (*sections, 0, 0, 0)[:4]
     if q_out is None:
-        q_out = torch.empty((B, T, H_q, d), dtype=q.dtype, device=q.device)
-    if q_out.dtype != q.dtype:
+        q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+    if q_out.dtype is not dtype:
         raise TypeError("q_out must have q's dtype")
-    _one_shape((B, T, H_q, d), q_out=q_out)
-    _one_type(torch.float32, inv_freq=inv_freq, q_norm=q_norm, k_norm=k_norm)
-    _one_shape((rot // 2,), inv_freq=inv_freq)
-    _one_shape((d,), q_norm=q_norm, k_norm=k_norm)
-    _one_type(torch.int64, slot_map=slot_map)
-    _one_shape((B, T), slot_map=slot_map)
+    if q_out.shape != q_shape:
+        raise ValueError("q_out must be %s, not %s" % (list(q_shape), list(q_out.shape)))
+    if k.get_device() != dev or v.get_device() != dev or q_out.get_device() != dev:
+        raise ValueError("k, v and q_out are not where q is")
     if positions is not None:
-        _one_type(torch.int32, positions=positions)
-        _one_shape((len(sections), B, T), positions=positions)
         kv_len = q_len = None
-    else:
-        _one_type(torch.int32, kv_len=kv_len, q_len=q_len)
-        _one_shape((B,), kv_len=kv_len, q_len=q_len)
-    dt = _dtype_code(q.dtype)
-    sh = _kv_shape(B, T, H_q, H_kv, d, dt, dt, k_cache.shape[1], k_cache.shape[0], 1, strides, status_word)
-    rp = _Rope(rot, len(sections), (ctypes.c_int32 * 4)(*sections), int(bool(axes_interleaved)), int(bool(pairs_interleaved)),
-               float(norm_eps), _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
-               _token_stride("q_out", q_out))
-    pq, pk, pv, po, pkc, pvc = _strided_ptrs(q, k, v, q_out, k_cache, v_cache)
-    _check(_load().gdn_rope_append(ctypes.byref(sh), ctypes.byref(rp), pq, pk, pv,
-                                   *_ptrs(inv_freq, positions, kv_len, q_len, slot_map, q_norm, k_norm), po, pkc, pvc,
-                                   _stream(stream)))
+    per, heads = (B,), (d,)
+    args = (_want("inv_freq", inv_freq, _F32, (half,), dev), _want("positions", positions, _I32, (n_axes, B, T), dev),
+            _want("kv_len", kv_len, _I32, per, dev), _want("q_len", q_len, _I32, per, dev),
+            _want("slot_map", slot_map, _I64, (B, T), dev), _want("q_norm", q_norm, _F32, heads, dev),
+            _want("k_norm", k_norm, _F32, heads, dev))
+    code = _dtype_code(dtype)
+    status = _want("status_word", status_word, _I32, (1,), dev) or 0
+    shape = _pack_kv_shape(B, T, H_q, H_kv, d, code, code, page, pages, 1, st[0], st[1], st[2], status)
+    rope = _pack_rope(2 * half, n_axes, *sec, 1 if axes_interleaved else 0, 1 if pairs_interleaved else 0, norm_eps,
+                      _token_stride("q", q, B, T, H_q, d), _token_stride("k", k, B, T, H_kv, d),
+                      _token_stride("v", v, B, T, H_kv, d), _token_stride("q_out", q_out, B, T, H_q, d))
+    rc = _load().gdn_rope_append(shape, rope, q.data_ptr(), k.data_ptr(), v.data_ptr(), *args, q_out.data_ptr(),
+                                 k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return q_out
 
 
 def paged_attention_workspace_bytes(B, T, H_q, H_kv, d, dtype=torch.bfloat16) -> int:
     """Bytes of workspace :func:`paged_attention` needs."""
-    dt = _dtype_code(dtype)
-    sh = _KvShape(B, T, H_q, H_kv, d, dt, dt, 1, 1, 1, 0, 0, 0, None)
-    return int(_load().gdn_paged_attention_workspace_bytes(ctypes.byref(sh)))
+    code = _dtype_code(dtype)
+    return int(_load().gdn_paged_attention_workspace_bytes(_pack_kv_shape(B, T, H_q, H_kv, d, code, code, 1, 1, 1, 0, 0, 0, 0)))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=None, window=0, o=None, lse=None,
@@ -653,28 +648,31 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=
     sequence whose pages block_table [B, max_pages] lists, and sees up to itself (``window`` > 0: that
     many positions at most). ``scale`` defaults to d ** -0.5; ``lse`` [B, T, H_q] fp32 receives
     the log of the softmax's sum. Returns o (``out_dtype``, default q's)."""
-    B, T, H_q, d = q.shape
+    B, T, H_q, d = q_shape = q.shape
+    dtype, dev = q.dtype, q.get_device()
     H_kv = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    strides = _cache_strides(k_cache, v_cache, H_kv, d, q.dtype)
+    page, pages, st = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
     if o is None:
-        o = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    elif out_dtype is not None and o.dtype != out_dtype:
+        o = torch.empty(q_shape, dtype=out_dtype or dtype, device=q.device)
+    elif out_dtype is not None and o.dtype is not out_dtype:
         raise TypeError("o is %s but out_dtype is %s" % (o.dtype, out_dtype))
-    _one_shape((B, T, H_q, d), o=o)
-    _one_type(torch.float32, lse=lse)
-    _one_shape((B, T, H_q), lse=lse)
-    _one_type(torch.int32, block_table=block_table, kv_len=kv_len, q_len=q_len)
-    _one_shape((B,), kv_len=kv_len, q_len=q_len)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    sh = _kv_shape(B, T, H_q, H_kv, d, _dtype_code(q.dtype), _dtype_code(o.dtype), k_cache.shape[1], k_cache.shape[0],
-                   block_table.shape[1], strides, status_word)
+    per = (B,)
+    args = (_want("block_table", block_table, _I32, table_shape, dev), _want("kv_len", kv_len, _I32, per, dev),
+            _want("q_len", q_len, _I32, per, dev), _want("o", o, o.dtype, q_shape, dev),
+            _want("lse", lse, _F32, (B, T, H_q), dev))
+    p_q = _want("q", q, dtype, q_shape, dev)
+    status = _want("status_word", status_word, _I32, (1,), dev) or 0
+    shape = _pack_kv_shape(B, T, H_q, H_kv, d, _dtype_code(dtype), _dtype_code(o.dtype), page, pages, table_shape[1],
+                           st[0], st[1], st[2], status)
     lib = _load()
     if workspace is None:
-        need = lib.gdn_paged_attention_workspace_bytes(ctypes.byref(sh))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    kc, vc = _strided_ptrs(k_cache, v_cache)
-    pq, *rest = _ptrs(q, block_table, kv_len, q_len, o, lse, workspace)
-    _check(lib.gdn_paged_attention(ctypes.byref(sh), d ** -0.5 if scale is None else float(scale), int(window), pq, kc, vc,
-                                   *rest, _nbytes(workspace), _stream(stream)))
+        workspace = torch.empty(max(lib.gdn_paged_attention_workspace_bytes(shape), 16), dtype=torch.uint8, device=q.device)
+    p_ws = _want("workspace", workspace, workspace.dtype, workspace.shape, dev)
+    rc = lib.gdn_paged_attention(shape, d ** -0.5 if scale is None else scale, window, p_q, k_cache.data_ptr(),
+                                 v_cache.data_ptr(), *args, p_ws, _nbytes(workspace), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return o

@@ -1,7 +1,5 @@
 """Refusals of the paged attention calls, made on the host before any launch (no GPU needed:
 nothing here is ever launched)."""
-import ctypes
-
 import pytest
 import torch
 
@@ -21,9 +19,9 @@ def gdn():
 
 def _shape(gdn, **kw):
     f = dict(B=2, T=8, H_q=24, H_kv=4, d=128, dtype=BF16, out_dtype=BF16, page_size=16, num_pages=100, max_pages=8,
-             page_stride=16 * 4 * 128, slot_stride=4 * 128, head_stride=128, status_word=None)
+             page_stride=16 * 4 * 128, slot_stride=4 * 128, head_stride=128, status_word=0)
     f.update(kw)
-    return gdn._KvShape(*f.values())
+    return gdn._pack_kv_shape(*f.values())
 
 
 def _err(gdn):
@@ -40,7 +38,7 @@ def test_plan_refusals(gdn):
         at = {n: FAKE * (i + 1) for i, n in enumerate(names)}
         at.update(seq_out=at["seq_in"], held_out=at["held_in"], count_out=at["count_in"])
         at.update(kw)
-        return lib.gdn_kv_plan(ctypes.byref(shape or _shape(gdn)), *[at[n] for n in names], None)
+        return lib.gdn_kv_plan(shape or _shape(gdn), *[at[n] for n in names], None)
 
     assert lib.gdn_kv_plan(None, *([FAKE] * 14), None) == INVALID
     for bad in (dict(B=-1), dict(T=0), dict(page_size=0), dict(num_pages=0), dict(max_pages=0)):
@@ -61,16 +59,17 @@ def test_plan_refusals(gdn):
 
 def test_append_refusals(gdn):
     lib = gdn.lib()
-    rope = lambda **kw: gdn._Rope(*dict(dict(  # noqa: E731
-        rot=128, n_axes=3, sections=(ctypes.c_int32 * 4)(32, 16, 16, 0), ai=0, pi=0, eps=1e-6, q=24 * 128, k=4 * 128,
-        v=4 * 128, o=24 * 128), **kw).values())
+    def rope(**kw):
+        f = dict(dict(rot=128, n_axes=3, sections=(32, 16, 16, 0), ai=0, pi=0, eps=1e-6, q=24 * 128, k=4 * 128, v=4 * 128,
+                      o=24 * 128), **kw)
+        return gdn._pack_rope(f["rot"], f["n_axes"], *f["sections"], *list(f.values())[3:])
 
     def call(shape=None, r=None, **kw):
         names = ["q", "k", "v", "inv_freq", "positions", "kv_len", "q_len", "slots", "q_norm", "k_norm", "q_out", "k_cache",
                  "v_cache"]
         at = {n: FAKE * (i + 1) for i, n in enumerate(names)}
         at.update(kw)
-        return lib.gdn_rope_append(ctypes.byref(shape or _shape(gdn)), ctypes.byref(r or rope()), *[at[n] for n in names], None)
+        return lib.gdn_rope_append(shape or _shape(gdn), r or rope(), *[at[n] for n in names], None)
 
     assert call(_shape(gdn, H_q=23)) == INVALID and "multiple of H_kv" in _err(gdn)
     assert call(_shape(gdn, d=96)) == UNSUP and "not built" in _err(gdn)
@@ -79,12 +78,12 @@ def test_append_refusals(gdn):
     for s in ("page_stride", "slot_stride", "head_stride"):
         assert call(_shape(gdn, **{s: 64})) == INVALID and s in _err(gdn)            # less than d
         assert call(_shape(gdn, **{s: 4 * 128 + 4})) == INVALID and s in _err(gdn)   # not 16 bytes
-    sec = lambda *v: (ctypes.c_int32 * 4)(*v)  # noqa: E731
+    sec = lambda *v: v  # noqa: E731
     for bad in (dict(rot=8), dict(rot=24), dict(rot=144), dict(n_axes=0), dict(n_axes=5), dict(sections=sec(32, 16, 15, 0)),
                 dict(sections=sec(80, -16, 0, 0)), dict(ai=2), dict(pi=-1), dict(eps=-1.0), dict(eps=float("nan")),
                 dict(ai=1, sections=sec(2, 30, 32, 0)), dict(q=24 * 128 - 8), dict(k=4 * 128 + 4), dict(v=0), dict(o=128)):
         assert call(r=rope(**bad)) == INVALID, bad
-    assert lib.gdn_rope_append(ctypes.byref(_shape(gdn)), None, *([FAKE] * 13), None) == INVALID
+    assert lib.gdn_rope_append(_shape(gdn), None, *([FAKE] * 13), None) == INVALID
     for n in ("q", "k", "v", "inv_freq", "slots", "q_out", "k_cache", "v_cache"):
         assert call(**{n: None}) == INVALID and "is NULL" in _err(gdn), n
     assert call(positions=None, kv_len=None) == INVALID and "kv_len is NULL" in _err(gdn)
@@ -103,7 +102,7 @@ def test_attention_refusals(gdn):
         names = ["q", "k", "v", "table", "kv_len", "q_len", "o", "lse", "ws"]
         at = {n: FAKE * (i + 1) for i, n in enumerate(names)}
         at.update(kw)
-        return lib.gdn_paged_attention(ctypes.byref(shape or _shape(gdn)), scale, window, *[at[n] for n in names], nbytes, None)
+        return lib.gdn_paged_attention(shape or _shape(gdn), scale, window, *[at[n] for n in names], nbytes, None)
 
     for bad, want in ((dict(T=17), UNSUP), (dict(T=0), INVALID), (dict(B=65536), UNSUP), (dict(d=80), UNSUP), (dict(H_q=25), INVALID),
                       (dict(dtype=3), INVALID), (dict(out_dtype=3), INVALID), (dict(max_pages=0), INVALID),
