@@ -4,11 +4,12 @@
 // Every element of q, k and v is read once and written once; the angles of a token (rot / 2 of
 // them) are the same for all its heads, so a CTA forms them once in shared memory: the product
 // position x frequency in fp64, reduced to a fraction of a turn there, cosine and sine in fp32.
-// Bound by HBM for prompts, by latency for a block of a few tokens.
+// Measured for 24,576 tokens of 48 heads, d 128, bf16, head norms, three axes (604 MB): 144 us, 64% of
+// the measured copy rate; the same kernel without its arithmetic takes 109 us, without the norm 128 us, without
+// the cosines no less; with 8 tokens per CTA 151 us, with 4 167 us, with 32 169 us. So it is bound by issue and HBM together. A block of a few tokens (8 x 32
+// heads, d 256) takes 3.5 us, launch and three dependent reads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-
-#include <algorithm>
 
 #include "gdn_device.cuh"
 #include "gdn_internal.cuh"
@@ -18,225 +19,227 @@ namespace {
 
 using namespace dev;
 
-constexpr int kMaxThreads = 256;
-constexpr int kManyTokens = 148 * 8;   // from here on a CTA takes four tokens
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Tokens from which on a CTA takes four, and sixteen. Measured with one, four, sixteen tokens per CTA (48 heads,
+// d 128, norms): 128 tokens 4.0, 8.1, 22 us; 256 6.3, 8.2, 23; 512 10.9, 8.4, 23; 4096 81, 30, 40; 8192
+// 163, 57, 52; 16,384 337, 104, 99 (20 heads, d 256, 8192 tokens: 160, 44, 39).
+constexpr int kFour = 320, kSixteen = 6144;
 
-// Eight elements as stored, and as fp32.
+// Four elements as stored, and as fp32.
 template <typename E>
-struct Raw8;
+struct Raw4;
 template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 u;
+struct Raw4<__nv_bfloat16> {
+    uint2 u;
 };
 template <>
-struct Raw8<float> {
-    float4 a, b;
+struct Raw4<float> {
+    float4 u;
 };
-
 // A plain load: q may be rotated in place, so the read-only path is not used.
-__device__ __forceinline__ void load(const __nv_bfloat16* p, Raw8<__nv_bfloat16>& r) {
-    r.u = *reinterpret_cast<const uint4*>(p);
+template <typename E>
+__device__ __forceinline__ void load(const E* p, Raw4<E>& r) {
+    r.u = *reinterpret_cast<const decltype(Raw4<E>::u)*>(p);
 }
-__device__ __forceinline__ void load(const float* p, Raw8<float>& r) {
-    r.a = reinterpret_cast<const float4*>(p)[0];
-    r.b = reinterpret_cast<const float4*>(p)[1];
+template <typename E>
+__device__ __forceinline__ void store(E* p, const Raw4<E>& r) {
+    *reinterpret_cast<decltype(Raw4<E>::u)*>(p) = r.u;
 }
-__device__ __forceinline__ void store(__nv_bfloat16* p, const Raw8<__nv_bfloat16>& r) {
-    *reinterpret_cast<uint4*>(p) = r.u;
+__device__ __forceinline__ void unpack(const Raw4<__nv_bfloat16>& r, float (&x)[4]) {
+    x[0] = __uint_as_float(r.u.x << 16);
+    x[1] = __uint_as_float(r.u.x & 0xffff0000u);
+    x[2] = __uint_as_float(r.u.y << 16);
+    x[3] = __uint_as_float(r.u.y & 0xffff0000u);
 }
-__device__ __forceinline__ void store(float* p, const Raw8<float>& r) {
-    reinterpret_cast<float4*>(p)[0] = r.a;
-    reinterpret_cast<float4*>(p)[1] = r.b;
+__device__ __forceinline__ void unpack(const Raw4<float>& r, float (&x)[4]) {
+    x[0] = r.u.x, x[1] = r.u.y, x[2] = r.u.z, x[3] = r.u.w;
 }
-__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
-    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
+__device__ __forceinline__ void pack(const float (&x)[4], Raw4<__nv_bfloat16>& r) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    r.u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&x)[8]) {
-    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-}
-__device__ __forceinline__ void pack(const float (&x)[8], Raw8<__nv_bfloat16>& r) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    r.u = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void pack(const float (&x)[8], Raw8<float>& r) {
-    r.a = make_float4(x[0], x[1], x[2], x[3]);
-    r.b = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void pack(const float (&x)[4], Raw4<float>& r) { r.u = make_float4(x[0], x[1], x[2], x[3]); }
+
+// The pair (a, b) turned by an angle.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = a;
+    a = x * c - b * s;
+    b = x * s + b * c;
 }
 
-// grid (groups of TT tokens, groups of rows); a row is one head of q, k or v, d / 8 lanes each hold eight
-// of its elements, so a lane's cosines and sines are the same for all rows of a token and stay in
-// registers. The next token's rows (ITER for each lane) are in flight while this one's are worked on.
+// The first element of a token's slot within a head's stride, or -1 where it has none.
+__device__ __forceinline__ int64_t cell_of(const RopeArgs& a, int tok, bool report) {
+    const int64_t slot = a.slots[tok], slots = (int64_t)a.cache.num_pages * a.cache.page;
+    if (slot < 0 || slot >= slots) {
+        if (slot >= slots && report && a.status_word) atomicOr(a.status_word, kStatusBadPage);
+        return -1;
+    }
+    const int64_t page = slots >> 32 ? slot / a.cache.page : (uint32_t)slot / (uint32_t)a.cache.page;
+    return page * a.cache.page_stride + (slot - page * a.cache.page) * a.cache.slot_stride;
+}
+
+// grid (groups of TT tokens, groups of heads, 1 or 3): a CTA takes q, k and v one after the other (few tokens: one
+// of them), so that pointers, strides and norm are the same for all its threads. A row is one head; d / 8
+// lanes hold eight of its elements each, in two quarters so chosen that the partners of a lane's elements
+// are its own: elements 4 l and rot / 2 + 4 l on for halves, 8 l on for neighbouring pairs and behind rot.
+// So nothing crosses lanes but the norm's sum, a lane's norm weights stay in registers for all its rows,
+// and its cosines and sines for a token's. Eight warps take a token's rows, ITER for each lane, or several
+// tokens' at once where a token has few.
 template <typename E, int D, int ITER, int TT>
-__global__ void __launch_bounds__(kMaxThreads) gdn_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) gdn_rope_append_kernel(const __grid_constant__ RopeArgs a, int heads_per_cta) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     __shared__ alignas(16) float s_cos[TT][D / 2], s_sin[TT][D / 2];
-    __shared__ int64_t s_cell[TT];   // the slot's first element within a head's stride, or -1
-    const int tokens = a.B * a.T, tok0 = blockIdx.x * TT;
+    __shared__ int64_t s_cell[TT];
+    const int tokens = a.B * a.T, tok0 = blockIdx.x * TT, head0 = blockIdx.y * heads_per_cta;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane % LPR;
-    const int rows = a.Hq + 2 * a.Hk, step = (blockDim.x >> 5) * RPW;
-    const int r0 = blockIdx.y * (step * ITER) + warp * RPW + lane / LPR;
     const int half = a.rot / 2;
+    const bool turned = 8 * l < a.rot, halves = turned && !a.pairs_interleaved;
+    const int o1 = halves ? 4 * l : 8 * l, o2 = halves ? half + 4 * l : 8 * l + 4;   // where the quarters begin
 
-    Raw8<E> raw[2][ITER];
-    auto fetch = [&](int tok, Raw8<E>(&to)[ITER]) {
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int r = r0 + i * step;
-            const E* p = nullptr;
-            if (r < a.Hq) p = static_cast<const E*>(a.q) + (int64_t)tok * a.q_stride + (int64_t)r * D;
-            else if (r < a.Hq + a.Hk) p = static_cast<const E*>(a.k) + (int64_t)tok * a.k_stride + (int64_t)(r - a.Hq) * D;
-            else if (r < rows) p = static_cast<const E*>(a.v) + (int64_t)tok * a.v_stride + (int64_t)(r - a.Hq - a.Hk) * D;
-            to[i] = Raw8<E>{};
-            if (p) load(p + 8 * l, to[i]);
-        }
-    };
-    fetch(tok0, raw[0]);
-
-    for (int i = tid; i < TT * half; i += blockDim.x) {
-        const int tt = i / half, e = i - tt * half, tok = tok0 + tt;
-        if (tok >= tokens) break;
-        int axis = 0;
-        if (a.axes_interleaved) {
-            axis = e % a.axes;
-            if (e >= a.axes * a.sections[axis]) axis = 0;
-        } else {
-            int end = a.sections[0];
-            while (e >= end) end += a.sections[++axis];   // the sections hold half pairs in all
-        }
-        int64_t pos;
-        if (a.positions) {
-            pos = a.positions[(int64_t)axis * tokens + tok];
-        } else {
-            const int b = tok / a.T;
-            pos = (int64_t)a.kv_len[b] - a.q_len[b] + (tok - b * a.T);
-        }
-        // turns = pos f / 2 pi, its whole part taken off in fp64; what is left is rounded to
-        // fp32 once (half a step, 2^-24 of at most half a turn: 2e-7 in angle)
-        double turns = (double)pos * (double)a.inv_freq[e] * 0.15915494309189535;
-        turns -= rint(turns);
-        sincospif(2.f * (float)turns, &s_sin[tt][e], &s_cos[tt][e]);
-    }
-    if (tid < TT) {
-        int64_t cell = -1;
-        if (tok0 + tid < tokens) {
-            const int64_t slot = a.slots[tok0 + tid];
-            const int64_t slots = (int64_t)a.cache.num_pages * a.cache.page;
-            if (slot >= 0 && slot < slots) {
-                const int64_t page = slots >> 32 ? slot / a.cache.page : (uint32_t)slot / (uint32_t)a.cache.page;
-                cell = page * a.cache.page_stride + (slot - page * a.cache.page) * a.cache.slot_stride;
-            } else if (slot >= slots && a.status_word) {
-                atomicOr(a.status_word, kStatusBadPage);
+    if (tid < TT) s_cell[tid] = tok0 + tid < tokens ? cell_of(a, tok0 + tid, blockIdx.z == 0 && head0 == 0) : -1;
+    if (blockIdx.z < 2)
+        for (int i = tid; i < (TT == 1 ? half : kThreads / half * half); i += kThreads) {   // pairs x tokens abreast
+            const int e = i % half, t_step = kThreads / half;
+            int axis = 0;
+            if (a.axes_interleaved) {
+                axis = e % a.axes;
+                if (e >= a.axes * a.sections[axis]) axis = 0;
+            } else {
+                int end = a.sections[0];
+                while (e >= end) end += a.sections[++axis];   // the sections hold half pairs in all
+            }
+            const double f = (double)a.inv_freq[e];
+            for (int tt = i / half; tt < TT && tok0 + tt < tokens; tt += t_step) {
+                const int tok = tok0 + tt;
+                int pos;                                      // kv_len - q_len + t is below 2^30 + 2^20
+                if (a.positions) {
+                    pos = a.positions[(int64_t)axis * tokens + tok];
+                } else {
+                    const int b = tok / a.T;
+                    pos = a.kv_len[b] - a.q_len[b] + (tok - b * a.T);
+                }
+                // turns = pos f / 2 pi, its whole part taken off in fp64; what is left is rounded to
+                // fp32 once (half a step, 2^-24 of at most half a turn: 2e-7 in angle)
+                double turns = (double)pos * f * 0.15915494309189535;
+                turns -= rint(turns);
+                sincospif(2.f * (float)turns, &s_sin[tt][e], &s_cos[tt][e]);
             }
         }
-        s_cell[tid] = cell;
-    }
     __syncthreads();
 
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) {
-        const int tok = tok0 + tt;
-        if (tt + 1 < TT && tok + 1 < tokens) fetch(tok + 1, raw[(tt + 1) & 1]);
-        const int64_t cell = s_cell[tt];
-        if (cell < 0) continue;                              // no slot: nothing of this token is written
-        // this lane's eight angles' cosines and sines (interleaved: four pairs; else the first or the
-        // second element of eight)
-        const bool turned = 8 * l < a.rot, first = 8 * l < half;
-        float cs[8], sn[8];
-        const int at = !turned ? 0 : a.pairs_interleaved ? 4 * l : first ? 8 * l : 8 * l - half;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const int i = a.pairs_interleaved ? at : at + e;
-            const float4 c4 = *reinterpret_cast<const float4*>(&s_cos[tt][i]), s4 = *reinterpret_cast<const float4*>(&s_sin[tt][i]);
-            cs[e] = c4.x, cs[e + 1] = c4.y, cs[e + 2] = c4.z, cs[e + 3] = c4.w;
-            sn[e] = s4.x, sn[e + 1] = s4.y, sn[e + 2] = s4.z, sn[e + 3] = s4.w;
+    for (int what = blockIdx.z; what < 3; what += gridDim.z) {
+        const int all_heads = what == 0 ? a.Hq : a.Hk;
+        if (head0 >= all_heads) continue;
+        const int heads = min(heads_per_cta, all_heads - head0);
+        const int64_t stride = what == 0 ? a.q_stride : what == 1 ? a.k_stride : a.v_stride;
+        const E* src = static_cast<const E*>(what == 0 ? a.q : what == 1 ? a.k : a.v) + tok0 * stride + head0 * D;
+        const int64_t h_stride = what == 0 ? D : a.cache.head_stride;
+        E* dst = static_cast<E*>(what == 0 ? a.q_out : what == 1 ? a.cache.k : a.cache.v) + head0 * h_stride;
+        // this warp's rows: groups of RPW heads, from group on, and its tokens: from t0 on, abreast apart
+        const int groups = (heads + RPW - 1) / RPW, abreast = max(1, kWarps / groups);
+        const int group = groups < kWarps ? warp % groups : warp, t0 = groups < kWarps ? warp / groups : 0;
+        const int h0 = group * RPW + lane / LPR;
+        if (t0 >= abreast) continue;
+        const float* norm = what == 0 ? a.q_norm : what == 1 ? a.k_norm : nullptr;
+        float w1[4], w2[4];
+        if (norm) {
+            unpack(Raw4<float>{__ldg(reinterpret_cast<const float4*>(norm + o1))}, w1);
+            unpack(Raw4<float>{__ldg(reinterpret_cast<const float4*>(norm + o2))}, w2);
         }
+#pragma unroll 1
+        for (int tt = t0; tt < TT; tt += abreast) {
+            const int64_t cell = s_cell[tt];
+            if (cell < 0) continue;                          // no slot: nothing of this token is written
+            const E* from = src + tt * stride;
+            E* to = dst + (what == 0 ? (int64_t)(tok0 + tt) * a.qo_stride : cell);
+            Raw4<E> r1[ITER], r2[ITER];
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            Raw8<E>& w8 = raw[tt & 1][i];
-            const int r = r0 + i * step;
-            const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hk;
-            if (__any_sync(kFull, is_q || is_k)) {           // else a copy; every lane takes the shuffles
-                float x[8];
-                unpack(w8, x);
-                const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-                if (a.q_norm || a.k_norm) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                    ss = group_sum<LPR>(ss);
-                    if (w) {
-                        const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-                        const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + 8 * l));
-                        const float4 w1 = __ldg(reinterpret_cast<const float4*>(w + 8 * l) + 1);
-                        const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= inv * ww[e];
-                    }
+            for (int i = 0; i < ITER; ++i) {
+                const int h = h0 + i * (kWarps * RPW);
+                r1[i] = r2[i] = Raw4<E>{};
+                if (h < heads) {
+                    load(from + h * D + o1, r1[i]);
+                    load(from + h * D + o2, r2[i]);
                 }
-                if (a.pairs_interleaved) {
-                    if (turned) {
+            }
+            if (what < 2) {                                  // rows past the end take the shuffles too
+                float c[4], s[4];
+                const int at = !turned ? 0 : 4 * l;          // the lane's four pairs
+                unpack(Raw4<float>{*reinterpret_cast<const float4*>(&s_cos[tt][at])}, c);
+                unpack(Raw4<float>{*reinterpret_cast<const float4*>(&s_sin[tt][at])}, s);
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const float y = x[e];
-                            x[e] = y * cs[e / 2] - x[e + 1] * sn[e / 2];
-                            x[e + 1] = y * sn[e / 2] + x[e + 1] * cs[e / 2];
+                for (int i = 0; i < ITER; ++i) {
+                    if (group + i * kWarps >= groups) break;
+                    float x[4], y[4];
+                    unpack(r1[i], x);
+                    unpack(r2[i], y);
+                    if (norm) {
+                        float ss = x[0] * x[0], st = y[0] * y[0];
+#pragma unroll
+                        for (int e = 1; e < 4; ++e) {
+                            ss = fmaf(x[e], x[e], ss);
+                            st = fmaf(y[e], y[e], st);
+                        }
+                        const float inv = rsqrtf(group_sum<LPR>(ss + st) * (1.f / D) + a.eps);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] *= inv * w1[e];
+                            y[e] *= inv * w2[e];
                         }
                     }
-                } else {
-                    // rot / 2 is a multiple of 8: the eight partners are one lane's
-                    const int other = turned ? (first ? lane + half / 8 : lane - half / 8) : lane;
+                    if (turned) {
+                        if (a.pairs_interleaved) {
+                            turn(x[0], x[1], c[0], s[0]);
+                            turn(x[2], x[3], c[1], s[1]);
+                            turn(y[0], y[1], c[2], s[2]);
+                            turn(y[2], y[3], c[3], s[3]);
+                        } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float z = __shfl_sync(kFull, x[e], other);
-                        if (turned) x[e] = first ? x[e] * cs[e] - z * sn[e] : z * sn[e] + x[e] * cs[e];
+                            for (int e = 0; e < 4; ++e) turn(x[e], y[e], c[e], s[e]);
+                        }
                     }
+                    pack(x, r1[i]);
+                    pack(y, r2[i]);
                 }
-                if (is_q || is_k) pack(x, w8);
             }
-            if (r >= rows) continue;
-            E* to = is_q ? static_cast<E*>(a.q_out) + (int64_t)tok * a.qo_stride + (int64_t)r * D
-                         : static_cast<E*>(is_k ? a.cache.k : a.cache.v) + cell + (r - a.Hq - (is_k ? 0 : a.Hk)) * a.cache.head_stride;
-            store(to + 8 * l, w8);
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                const int h = h0 + i * (kWarps * RPW);
+                if (h < heads) {
+                    store(to + h * h_stride + o1, r1[i]);
+                    store(to + h * h_stride + o2, r2[i]);
+                }
+            }
         }
     }
 }
 
 template <typename E, int D, int ITER, int TT>
-cudaError_t launch(const RopeArgs& a, int warps, int groups, cudaStream_t stream) {
+cudaError_t launch(const RopeArgs& a, int heads_per_cta, cudaStream_t stream) {
     const unsigned tokens = (unsigned)a.B * (unsigned)a.T;
-    gdn_rope_append_kernel<E, D, ITER, TT><<<dim3((tokens + TT - 1) / TT, groups), 32 * warps, 0, stream>>>(a);
+    const dim3 grid((tokens + TT - 1) / TT, (a.Hq + heads_per_cta - 1) / heads_per_cta, TT == 1 ? 3 : 1);
+    gdn_rope_append_kernel<E, D, ITER, TT><<<grid, kThreads, 0, stream>>>(a, heads_per_cta);
     return cudaGetLastError();
+}
+
+template <typename E, int D, int TT>
+cudaError_t launch_iter(const RopeArgs& a, cudaStream_t stream) {
+    constexpr int STEP = kWarps * (32 / (D / 8));
+    const int iter = (a.Hq + STEP - 1) / STEP;
+    if (iter == 1) return launch<E, D, 1, TT>(a, STEP, stream);
+    if (iter == 2) return launch<E, D, 2, TT>(a, 2 * STEP, stream);
+    return launch<E, D, 3, TT>(a, 3 * STEP, stream);
 }
 
 template <typename E, int D>
 cudaError_t launch_rows(const RopeArgs& a, cudaStream_t stream) {
-    constexpr int RPW = 32 / (D / 8), kMaxWarps = kMaxThreads / 32;
-    const int units = (a.Hq + 2 * a.Hk + RPW - 1) / RPW;     // warps' worth of rows per token
+    constexpr int RPW = 32 / (D / 8), STEP = kWarps * RPW;   // heads that eight warps hold, one for each lane
+    // Few tokens: one row for each lane, so that a token's rows spread over as many SMs as they can. More:
+    // as many tokens per CTA as still give every SM its four CTAs.
     const int64_t tokens = (int64_t)a.B * a.T;
-    // Few tokens: one row for each lane, so that a token's rows spread over as many SMs as they can.
-    if (tokens < kManyTokens) {
-        const int warps = std::min(units, 4);
-        return launch<E, D, 1, 1>(a, warps, (units + warps - 1) / warps, stream);
-    }
-    // Many: rows per lane such that a CTA's warps hold a token, or as much of it as they can.
-    const int iter = std::min(4, (units + kMaxWarps - 1) / kMaxWarps);
-    const int groups = (units + kMaxWarps * iter - 1) / (kMaxWarps * iter);
-    const int warps = ((units + groups - 1) / groups + iter - 1) / iter;
-    if (iter == 1) return launch<E, D, 1, 4>(a, warps, groups, stream);
-    if (iter == 2) return launch<E, D, 2, 4>(a, warps, groups, stream);
-    if (iter == 3) return launch<E, D, 3, 4>(a, warps, groups, stream);
-    return launch<E, D, 4, 4>(a, warps, groups, stream);
+    if (tokens < kFour) return launch<E, D, 1, 1>(a, STEP, stream);
+    return tokens < kSixteen ? launch_iter<E, D, 4>(a, stream) : launch_iter<E, D, 16>(a, stream);
 }
 
 template <typename E>
