@@ -272,8 +272,9 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = gridDim.x, c = blockIdx.x, tile = blockIdx.y;
-    // the join kernel may take its place on the SMs now; it waits for this one to end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The join kernel may take its place on the SMs from here on; it waits for this one to end.
+    grid_wait();
+    grid_release();
     int kv0, rows0;
     ask_counts(a, kv0, rows0);
     const Start at = find_start<NT, G::kUnit, G::kExtra>(x, s_start, c, C, tile, kv0, rows0);
@@ -516,8 +517,8 @@ cudaError_t launch_stream(const Args& x, const Plan& p, cudaStream_t stream) {
     constexpr int bytes = G::kWarps * G::kRing + 16 * MT * G::kRow;
     cudaError_t e = ensure_smem_attr<gdn_paged_attention_kernel<E, D, MT>>(bytes);
     if (e != cudaSuccess) return e;
-    gdn_paged_attention_kernel<E, D, MT><<<dim3(p.ctas, p.tiles), G::kWarps * 32, bytes, stream>>>(x);
-    e = cudaGetLastError();
+    Launch l(dim3(p.ctas, p.tiles), G::kWarps * 32, bytes, stream);
+    e = cudaLaunchKernelEx(&l.cfg, gdn_paged_attention_kernel<E, D, MT>, x);
     return e != cudaSuccess ? e : launch_join(x, p, stream);
 }
 

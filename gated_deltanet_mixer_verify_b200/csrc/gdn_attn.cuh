@@ -25,6 +25,26 @@ constexpr int kMaxSms = 160;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Every kernel here is launched as a programmatic dependent: it may begin while the kernel before it on
+// the stream ends, waits for that one to complete before it reads or writes any global memory, and
+// lets the next one begin likewise.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+struct Launch {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    Launch(dim3 grid, int threads, int smem, cudaStream_t stream) : cfg{} {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+};
+
 // How one launch is laid out (host).
 struct Plan {
     int unit;       // positions per unit

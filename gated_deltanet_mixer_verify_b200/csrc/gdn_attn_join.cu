@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
     __shared__ float s_o[kWarps][D], s_m[kWarps], s_l[kWarps];
     const AttnArgs& a = x.a;
     const int G = a.Hq / a.Hk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
+    grid_release();
     const int64_t W = x.parts.units[0];
     // the split items, in the order of their leads
     int n = 0;
@@ -150,16 +151,8 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
 
 template <int D>
 cudaError_t launch(const Args& x, const Plan& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * kMaxSms);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_paged_attention_join_kernel<D>, x, p.ctas, x.a.Hq / x.a.Hk * x.a.T);
+    Launch l(dim3(2 * kMaxSms), kThreads, 0, stream);
+    return cudaLaunchKernelEx(&l.cfg, gdn_paged_attention_join_kernel<D>, x, p.ctas, x.a.Hq / x.a.Hk * x.a.T);
 }
 
 }  // namespace

@@ -178,11 +178,6 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = gridDim.x, c = blockIdx.x, mtile = blockIdx.y;
-    // the join kernel may take its place on the SMs now; it waits for this one to end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    int kv0, rows0;
-    ask_counts(a, kv0, rows0);
     const uint32_t raw = smem_u32(smem_raw), ring_at = (raw + 1023u) & ~1023u;
     unsigned char* const ring = smem_raw + (ring_at - raw);
     constexpr uint32_t kQOff = G::kSlots * kBlock, kPOff = kQOff + G::kQ;
@@ -213,6 +208,12 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     // rows of Q that are nobody's stay zero
     for (int i = tid; i < G::kQ / 16; i += G::kThreads) reinterpret_cast<uint4*>(ring + kQOff)[i] = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
+    // So far nothing was read that another kernel writes: this may run while the kernel before ends. The
+    // join kernel may take its place on the SMs from here on; it waits for this one to end.
+    grid_wait();
+    grid_release();
+    int kv0, rows0;
+    ask_counts(a, kv0, rows0);
     const Start at = find_start<G::kThreads, kTile, kExtra>(x, s_start, c, C, mtile, kv0, rows0);
     tc::fence_before_sync();
     __syncthreads();
@@ -391,12 +392,23 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                                 if (r >= from && r < to) o[r] += y;
                         }
                     }
+                    int64_t to[16];
+                    float f[16];
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int64_t to = s_row[wg][q * 16 + r];
-                        if (to < 0) continue;
-                        if (w.whole) store_o(a, to * D + col, o[r] * s_k[wg][q * 16 + r]);
-                        else x.parts.o[to * D + col] = o[r];
+                        to[r] = s_row[wg][q * 16 + r] < 0 ? -1 : s_row[wg][q * 16 + r] * D + col;
+                        f[r] = o[r] * s_k[wg][q * 16 + r];
+                    }
+                    if (!w.whole || !a.out_bf16) {
+                        float* out = w.whole ? static_cast<float*>(a.o) : x.parts.o;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (to[r] >= 0) out[to[r]] = f[r];
+                    } else {
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (to[r] >= 0) out[to[r]] = __float2bfloat16_rn(f[r]);
                     }
                 }
                 named_barrier_sync(bar, 128);                    // s_row, s_k and s_part are the next item's
@@ -631,8 +643,8 @@ cudaError_t launch(const Args& x, const Plan& p, cudaStream_t stream) {
         e = tc::encode_tmap_paged(&maps[i], i ? c.v : c.k, D, x.a.Hk, c.page, c.num_pages, c.head_stride, c.slot_stride,
                                   c.page_stride, run);
     if (e != cudaSuccess) return e;
-    gdn_paged_attention_tc_kernel<D, NB><<<dim3(p.ctas, p.tiles), G::kThreads, G::kBytes, stream>>>(x, maps[0], maps[1], run);
-    e = cudaGetLastError();
+    Launch l(dim3(p.ctas, p.tiles), G::kThreads, G::kBytes, stream);
+    e = cudaLaunchKernelEx(&l.cfg, gdn_paged_attention_tc_kernel<D, NB>, x, maps[0], maps[1], run);
     return e != cudaSuccess ? e : launch_join(x, p, stream);
 }
 template <int D>
