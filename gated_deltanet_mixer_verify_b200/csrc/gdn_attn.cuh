@@ -121,7 +121,7 @@ __device__ __forceinline__ Seq read_seq(const AttnArgs& a, int b, bool& bad) {
 // W units dealt to C CTAs: the first W % C get one more than the others.
 struct Deal {
     int64_t each, more;
-    __device__ __forceinline__ Deal(int64_t W, int C) : each(W / C), more(W - each * C) {}
+    __device__ __forceinline__ Deal(int64_t W, int C) : each(W >> 32 ? W / C : (uint32_t)W / (uint32_t)C), more(W - each * C) {}
     __device__ __forceinline__ int64_t first(int c) const { return c * each + min((int64_t)c, more); }
     __device__ __forceinline__ int cta_of(int64_t u) const {
         const int64_t t = more * (each + 1);
@@ -180,29 +180,30 @@ __device__ __forceinline__ Start find_start(const Args& x, int64_t* sm, int c, i
         }
         sm[NT / 32] = b;
         sm[NT / 32 + 1] = at;
-        if (C > 1 && tile == 0) {
-            Lead lead = {-1, 0, 0, 0};
-            const int h = (int)((s.u - at) / q.span);
-            const int64_t u0 = at + (int64_t)h * q.span;
+    }
+    __syncthreads();
+    s.b = (int)sm[NT / 32];
+    s.base = sm[NT / 32 + 1];
+    if (C > 1 && tile == 0 && tid == 0) {      // behind the barrier: nobody waits for it
+        Lead lead = {-1, 0, 0, 0};
+        if (s.u < s.end) {
+            bool bad;
+            const Seq q = read_seq<UNIT, EXTRA>(a, s.b, bad);
+            const int h = (int)((s.u - s.base) / q.span);
+            const int64_t u0 = s.base + (int64_t)h * q.span;
             if (s.u > u0 && s.u < u0 + q.units) {
                 const int c0 = deal.cta_of(u0);
                 if (deal.cta_of(s.u - 1) == c0) {
-                    lead.b = b;
+                    lead.b = s.b;
                     lead.h = h;
                     lead.c0 = c0;
                     lead.c1_slot = deal.cta_of(u0 + q.units - 1) * 2 + (deal.first(c0) == u0 ? 0 : 1);
                 }
             }
-            x.parts.lead[c] = lead;
         }
-    }
-    if (C > 1 && tile == 0 && tid == 0) {
-        if (s.u >= s.end) x.parts.lead[c] = Lead{-1, 0, 0, 0};
+        x.parts.lead[c] = lead;
         if (c == 0) x.parts.units[0] = W;
     }
-    __syncthreads();
-    s.b = (int)sm[NT / 32];
-    s.base = sm[NT / 32 + 1];
     return s;
 }
 // The counts of sequence threadIdx.x, for find_start.
