@@ -48,6 +48,7 @@ constexpr int kExtra = 2;                       // units that an item costs besi
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
+constexpr int kFetch = 2;                       // warps that fetch, every other block each
 constexpr int kMaskRing = 16;                   // more tiles than the ring holds, and the one in work
 
 // D columns of the head, NB blocks of 64 rows.
@@ -55,7 +56,7 @@ template <int D, int NB>
 struct Cfg {
     static constexpr int kGroups = 2 * NB;                            // of 128 threads and 32 rows
     static constexpr int kSoft = 128 * kGroups;                       // threads of the softmax
-    static constexpr int kThreads = kSoft + 96;
+    static constexpr int kThreads = kSoft + 32 * (kFetch + 2);
     static constexpr int kKb = D / 64;                                // ring blocks of a K or V tile
     static constexpr int kMb = D > 128 ? D / 128 : 1;                 // M = 128 blocks of O^T
     static constexpr int kQ = 64 * NB * D * 2;
@@ -201,7 +202,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         s_not_numbers = 0;
         s_ask = s_looked = 0;
     }
-    if (warp == kSoftWarps + 1) {
+    if (warp == kSoftWarps + kFetch) {
         tc::tmem_alloc(&s_tmem, G::kCols);
         tc::tmem_relinquish();
     }
@@ -417,8 +418,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);
         }
-    } else if (warp == kSoftWarps) {
+    } else if (warp < kSoftWarps + kFetch) {
         // ---------------------------------------------------------------- keys and values
+        // Two warps, because a lane that issues a copy takes 75 to 150 cycles for it, and a tile of short
+        // pages is many copies.
+        const uint32_t fw = warp - kSoftWarps;
         const int page = a.cache.page, runs = kTile / run;
         uint32_t issued = 0, g = 0;                  // blocks of the ring, tiles
         bool fine = true;
@@ -441,16 +445,28 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 if (need && a.status_word) atomicOr(a.status_word, kStatusBadPage);
                 return a.cache.num_pages;
             };
-            auto fetch = [&](const CUtensorMap* map, int j, int id) -> bool {
+            auto fetch = [&](const CUtensorMap* map, int j, int id, bool keys) -> bool {
                 const int slot0 = (first + j * kTile + lane * run) % page;
 #pragma unroll 1
-                for (int i = 0; i < G::kKb; ++i) {
+                for (int i = 0; i < G::kKb; ++i, ++issued) {
+                    if (issued % kFetch != fw) continue;
                     const uint32_t slot = issued % G::kSlots, round = issued / G::kSlots;
                     if (!await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, &s_lost)) return false;
+                    if (keys && i == 0) {
+                        // the tile's positions that are there, 32 to a word
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int bit = lane * run - 32 * q;             // this lane's run within the word
+                            uint32_t bits = 0;
+                            if (lane < runs && id < a.cache.num_pages && bit < 32 && bit + run > 0)
+                                bits = run >= 32 ? ~0u : ((1u << run) - 1) << bit;
+                            bits = __reduce_or_sync(kFull, bits);
+                            if (lane == 0) s_mask[g % kMaskRing][q] = bits;
+                        }
+                    }
                     if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], kBlock);
                     __syncwarp();
                     if (lane < runs) tc::tma_load_4d(ring + slot * kBlock + lane * run * 128, map, i * 64, w.h, slot0, id, &bars.kv_full[slot]);
-                    ++issued;
                 }
                 return true;
             };
@@ -459,20 +475,10 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             for (int j = 0; j <= n; ++j) {
                 if (j < n) {
                     id_k = page_of(j, id_k);
-                    // the tile's positions that are there, 32 to a word
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int bit = lane * run - 32 * q;     // this lane's run within the word
-                        uint32_t bits = 0;
-                        if (lane < runs && id_k < a.cache.num_pages && bit < 32 && bit + run > 0)
-                            bits = run >= 32 ? ~0u : ((1u << run) - 1) << bit;
-                        bits = __reduce_or_sync(kFull, bits);
-                        if (lane == 0) s_mask[g % kMaskRing][q] = bits;
-                    }
+                    if (!(fine = fetch(&k_map, j, id_k, true))) break;
                     ++g;
-                    if (!(fine = fetch(&k_map, j, id_k))) break;
                 }
-                if (j > 0 && !(fine = fetch(&v_map, j - 1, id_v))) break;
+                if (j > 0 && !(fine = fetch(&v_map, j - 1, id_v, false))) break;
                 id_v = id_k;
                 id_k = id_next;
                 id_next = look_up(j + 2);
@@ -481,9 +487,10 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         if (!fine) {
             // given up: let the copies in flight land before the shared memory goes
             for (uint32_t s = issued > G::kSlots ? issued - G::kSlots : 0; s < issued; ++s)
+                if (s % kFetch == fw)
                 for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.kv_full[s % G::kSlots], (s / G::kSlots) & 1); ++i) {}
         }
-    } else if (warp == kSoftWarps + 1) {
+    } else if (warp == kSoftWarps + kFetch) {
         // ---------------------------------------------------------------- products
         // The whole warp walks and waits alike and one elected lane issues: what the products take (addresses,
         // descriptors) is then the same in every lane by construction, and stays in uniform registers. A
@@ -627,7 +634,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kSoftWarps + 1) tc::tmem_dealloc(tmem, G::kCols);
+    if (warp == kSoftWarps + kFetch) tc::tmem_dealloc(tmem, G::kCols);
     if (tid == 0 && s_lost && a.status_word) atomicOr(a.status_word, kStatusWaitTimeout);
 }
 
