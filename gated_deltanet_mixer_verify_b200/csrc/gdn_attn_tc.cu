@@ -48,7 +48,7 @@ constexpr int kExtra = 2;                       // units that an item costs besi
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
-constexpr int kFetch = 2;                       // warps that fetch, every other block each
+constexpr int kFetch = 2;                       // warps that fetch, every other slot each
 constexpr int kMaskRing = 16;                   // more tiles than the ring holds, and the one in work
 
 // D columns of the head, NB blocks of 64 rows.
@@ -57,20 +57,23 @@ struct Cfg {
     static constexpr int kGroups = 2 * NB;                            // of 128 threads and 32 rows
     static constexpr int kSoft = 128 * kGroups;                       // threads of the softmax
     static constexpr int kThreads = kSoft + 32 * (kFetch + 2);
-    static constexpr int kKb = D / 64;                                // ring blocks of a K or V tile
+    static constexpr int kKb = D / 64;                                // blocks of 64 columns of a K or V tile
     static constexpr int kMb = D > 128 ? D / 128 : 1;                 // M = 128 blocks of O^T
+    static constexpr int kPer = kKb / kMb;                            // blocks of a ring slot: what one of them takes of V
+    static constexpr int kSlot = kPer * kBlock;
     static constexpr int kQ = 64 * NB * D * 2;
     static constexpr int kP = NB * kBlock;                            // one term of P
-    // even where a V operand spans two blocks, which must follow one another
-    static constexpr int kSlots = D == 256 ? (NB == 1 ? 8 : 4) : D == 128 ? (NB == 1 ? 10 : 6) : (NB == 1 ? 11 : 8);
-    static constexpr int kBytes = kSlots * kBlock + kQ + 2 * kP + 1024;   // + alignment
+    // buffers of P: with two, a tile's weights are written while the product before still reads its own
+    static constexpr int kPb = NB == 1 && D <= 128 ? 2 : 1;
+    static constexpr int kSlots = D == 256 ? (NB == 1 ? 4 : 2) : D == 128 ? (NB == 1 ? 4 : 3) : 8;
+    static constexpr int kBytes = kSlots * kSlot + kQ + 2 * kPb * kP + 1024;   // + alignment
     static constexpr uint32_t kO = 2 * 64 * NB;                       // column of O^T behind two S^T
     static constexpr uint32_t kCols = 64 * NB * (2 + kMb) <= 256 ? 256 : 512;
     static constexpr int kCpr = D / 8;                                // 16-byte chunks per row of Q
 };
 
 struct Bars {
-    uint64_t kv_full[16], kv_empty[16], s_full[2], p_full, pv_done, o_free, q_full, q_empty, drain;
+    uint64_t kv_full[8], kv_empty[8], s_full[2], p_full[2], pv_done[2], o_free, q_full, q_empty, drain;
 };
 
 // Byte offset of 16-byte chunk ch of row r in a tile of `rows` rows: blocks of 64 columns, 128-byte
@@ -181,7 +184,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     const int C = gridDim.x, c = blockIdx.x, mtile = blockIdx.y;
     const uint32_t raw = smem_u32(smem_raw), ring_at = (raw + 1023u) & ~1023u;
     unsigned char* const ring = smem_raw + (ring_at - raw);
-    constexpr uint32_t kQOff = G::kSlots * kBlock, kPOff = kQOff + G::kQ;
+    constexpr uint32_t kQOff = G::kSlots * G::kSlot, kPOff = kQOff + G::kQ;
     if (tid == 0) {
         tc::prefetch_tmap(&k_map);
         tc::prefetch_tmap(&v_map);
@@ -189,10 +192,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             mbar_init(&bars.kv_full[i], 1);
             mbar_init(&bars.kv_empty[i], 1);
         }
-        mbar_init(&bars.s_full[0], 2);
-        mbar_init(&bars.s_full[1], 2);
-        mbar_init(&bars.p_full, kSoftWarps);
-        mbar_init(&bars.pv_done, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 2);
+            mbar_init(&bars.p_full[i], kSoftWarps);
+            mbar_init(&bars.pv_done[i], 2);
+        }
         mbar_init(&bars.o_free, kSoftWarps);
         mbar_init(&bars.q_full, 1);
         mbar_init(&bars.q_empty, 1);
@@ -233,7 +237,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         const int my_row0 = row0 + 32 * wg;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float cs = x.c == 0.f ? 1.f : fabsf(x.c);
-        unsigned char* const P = ring + kPOff + (wg >> 1) * kBlock;
+        // the product of tile t is done
+        auto product_done = [&](uint32_t t) { return await_warp(&bars.pv_done[t & 1], (t >> 1) & 1, &s_lost); };
         uint32_t g = 0;                                          // tiles done by this CTA
         bool fine = true;
         float l[32];
@@ -295,9 +300,10 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         }
                         named_barrier_sync(bar, 128);
                     }
-                    // the product of the tile before still reads P, and O is rescaled behind it
-                    if (j > 0 && !(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) break;
+                    // the product that last read this buffer of P; and O is rescaled behind the one before
+                    if (j >= G::kPb && !(fine = product_done(g - G::kPb))) break;
                     if (move && j > 0) {
+                        if (!(fine = product_done(g - 1))) break;
                         tc::fence_after_sync();
 #pragma unroll
                         for (int r = 0; r < 32; ++r) l[r] *= s_k[wg][r];
@@ -312,6 +318,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         }
                         tc::tmem_st_wait();
                     }
+                    unsigned char* P = ring + kPOff + g % G::kPb * (2 * G::kP) + (wg >> 1) * kBlock;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {                // eight rows: one 16-byte chunk of each term
                         if (q >= 2 * chunks) break;
@@ -334,12 +341,12 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         *reinterpret_cast<uint4*>(P + G::kP + to_chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     tc::fence_proxy_async_smem();
-                } else if (j > 0 && !(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) {
+                } else if (j >= G::kPb && !(fine = product_done(g - G::kPb))) {
                     break;
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full);
+                if (lane == 0) mbar_arrive(&bars.p_full[g & 1]);
             }
             if (!fine) break;
             // the sums, and where the rows go
@@ -365,7 +372,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 }
                 named_barrier_sync(bar, 128);
             }
-            if (!(fine = await_warp(&bars.pv_done, (g - 1) & 1, &s_lost))) break;
+            if (!(fine = product_done(g - 1))) break;
             tc::fence_after_sync();
             if (chunks > 0) {
                 const bool repair = s_not_numbers != 0;
@@ -424,20 +431,21 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         // pages is many copies.
         const uint32_t fw = warp - kSoftWarps;
         const int page = a.cache.page, runs = kTile / run;
-        uint32_t issued = 0, g = 0;                  // blocks of the ring, tiles
+        const int r = lane % runs, blk = lane / runs;            // this lane's run of the tile, and its block of a slot
+        uint32_t issued = 0, g = 0;                  // slots of the ring, tiles
         bool fine = true;
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
-            // Lane i looks up the page of run i of tile j, and makes it num_pages (which TMA reads as zeros)
+            // A lane looks up the page of its run of tile j, and makes it num_pages (which TMA reads as zeros)
             // where nothing of the run is seen or the page is not in the pool.
             auto needed = [&](int j) -> bool {
-                const int pos = first + j * kTile + lane * run;
-                return lane < runs && j < n && pos < w.s.kv && pos + run > see.lo_min;
+                const int pos = first + j * kTile + r * run;
+                return j < n && pos < w.s.kv && pos + run > see.lo_min;
             };
             auto look_up = [&](int j) -> int {
-                return needed(j) ? a.table[(int64_t)w.b * a.max_pages + (first + j * kTile + lane * run) / page] : 0;
+                return needed(j) ? a.table[(int64_t)w.b * a.max_pages + (first + j * kTile + r * run) / page] : 0;
             };
             auto page_of = [&](int j, int id) -> int {
                 const bool need = needed(j);
@@ -446,9 +454,9 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 return a.cache.num_pages;
             };
             auto fetch = [&](const CUtensorMap* map, int j, int id, bool keys) -> bool {
-                const int slot0 = (first + j * kTile + lane * run) % page;
+                const int slot0 = (first + j * kTile + r * run) % page;
 #pragma unroll 1
-                for (int i = 0; i < G::kKb; ++i, ++issued) {
+                for (int i = 0; i < G::kMb; ++i, ++issued) {
                     if (issued % kFetch != fw) continue;
                     const uint32_t slot = issued % G::kSlots, round = issued / G::kSlots;
                     if (!await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, &s_lost)) return false;
@@ -456,17 +464,19 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         // the tile's positions that are there, 32 to a word
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int bit = lane * run - 32 * q;             // this lane's run within the word
+                            const int bit = r * run - 32 * q;                // this lane's run within the word
                             uint32_t bits = 0;
-                            if (lane < runs && id < a.cache.num_pages && bit < 32 && bit + run > 0)
+                            if (id < a.cache.num_pages && bit < 32 && bit + run > 0)
                                 bits = run >= 32 ? ~0u : ((1u << run) - 1) << bit;
                             bits = __reduce_or_sync(kFull, bits);
                             if (lane == 0) s_mask[g % kMaskRing][q] = bits;
                         }
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], kBlock);
+                    if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[slot], G::kSlot);
                     __syncwarp();
-                    if (lane < runs) tc::tma_load_4d(ring + slot * kBlock + lane * run * 128, map, i * 64, w.h, slot0, id, &bars.kv_full[slot]);
+                    if (blk < G::kPer)
+                        tc::tma_load_4d(ring + slot * G::kSlot + blk * kBlock + r * run * 128, map, (i * G::kPer + blk) * 64, w.h, slot0, id,
+                                        &bars.kv_full[slot]);
                 }
                 return true;
             };
@@ -493,13 +503,15 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     } else if (warp == kSoftWarps + kFetch) {
         // ---------------------------------------------------------------- products
         // The whole warp walks and waits alike and one elected lane issues: what the products take (addresses,
-        // descriptors) is then the same in every lane by construction, and stays in uniform registers. A
-        // single lane's own branch cost 90 to 140 cycles per product of 25.
+        // descriptors) is then the same in every lane by construction, and a run of products differs by
+        // constants only: 48 cycles each, where descriptors made one by one, or in a lane's own branch, cost
+        // 80 to 140. A wait costs 150 more, so there is one for each slot.
         const uint32_t tm = __shfl_sync(kFull, tmem, 0);
         const uint32_t N = (uint32_t)(rows + 15) / 16 * 16;
         const uint32_t id_s = tc::idesc_bf16(kTile, N, false), id_o = tc::idesc_bf16(128, N, true);
         uint32_t g = 0, items = 0, looked = 0;
-        uint32_t slot = 0, phase = 0;                            // of the ring: the next block
+        uint32_t slot = 0, phase = 0;                            // of the ring: the next one
+        const uint64_t q_at = tc::desc_kmajor_sw128(ring_at + kQOff), p_base = tc::desc_mnmajor_sw128(ring_at + kPOff, kBlock);
         bool fine = true;
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
@@ -509,18 +521,18 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             // S^T = K Q^T of tile j: into the buffer that tile j - 2's reader has left
             auto score = [&](int j) -> bool {
                 const uint32_t buf = (g + j) & 1;
-#pragma unroll 1
-                for (int kb = 0; kb < G::kKb; ++kb) {
+#pragma unroll
+                for (int mb = 0; mb < G::kMb; ++mb) {
                     if (!await_warp(&bars.kv_full[slot], phase, &s_lost)) return false;
                     tc::fence_after_sync();
                     if (elect_one()) {
-                        const uint32_t k_at = ring_at + slot * kBlock, q_at = ring_at + kQOff + kb * (64 * NB * 128);
+                        const uint64_t k_at = tc::desc_kmajor_sw128(ring_at + slot * G::kSlot);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc::mma_bf16_ss(tm + buf * (64 * NB), tc::desc_kmajor_sw128(k_at + i * 32), tc::desc_kmajor_sw128(q_at + i * 32),
-                                            id_s, kb > 0 || i > 0);
+                        for (int i = 0; i < 4 * G::kPer; ++i)
+                            tc::mma_bf16_ss(tm + buf * (64 * NB), k_at + ((i >> 2) * kBlock + (i & 3) * 32) / 16,
+                                            q_at + ((mb * G::kPer + (i >> 2)) * (64 * NB * 128) + (i & 3) * 32) / 16, id_s, mb > 0 || i > 0);
                         tc::mma_commit(&bars.kv_empty[slot]);
-                        if (kb == G::kKb - 1) {
+                        if (mb == G::kMb - 1) {
                             if (j == n - 1) tc::mma_commit(&bars.q_empty);
                             tc::mma_commit(&bars.s_full[buf]);
                             mbar_arrive(&bars.s_full[buf]);      // and what this warp has seen, the tile's mask among it
@@ -535,11 +547,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             for (int j = 0; j < n; ++j) {
                 if (j + 1 < n && !(fine = score(j + 1))) break;
                 // O^T += V^T P^T
-                if (!(fine = await_warp(&bars.p_full, (g + j) & 1, &s_lost))) break;
+                if (!(fine = await_warp(&bars.p_full[(g + j) & 1], ((g + j) >> 1) & 1, &s_lost))) break;
                 if (j == 0 && items > 0 && !(fine = await_warp(&bars.o_free, (items - 1) & 1, &s_lost))) break;
                 if (see.partial(first + j * kTile, kTile)) {
                     uint32_t sl = slot, ph = phase;
-                    for (int kb = 0; kb < G::kKb && fine; ++kb) {
+                    for (int mb = 0; mb < G::kMb && fine; ++mb) {
                         fine = await_warp(&bars.kv_full[sl], ph, &s_lost);
                         if (++sl == G::kSlots) sl = 0, ph ^= 1;
                     }
@@ -548,30 +560,26 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     if (lane == 0) set_count(&s_ask, looked);
                     if (!(fine = __all_sync(kFull, await_count(&s_looked, looked, &s_lost)))) break;
                 }
-                constexpr int per = G::kKb / G::kMb;             // blocks of 64 columns per product: 2, or 1 (d = 64)
-#pragma unroll 1
+                const uint64_t p_at = p_base + (g + j) % G::kPb * (2 * G::kP) / 16;
+#pragma unroll
                 for (int mb = 0; mb < G::kMb; ++mb) {
                     if (!(fine = await_warp(&bars.kv_full[slot], phase, &s_lost))) break;
-                    if (per == 2 && !(fine = await_warp(&bars.kv_full[slot + per - 1], phase, &s_lost))) break;
                     tc::fence_after_sync();
                     if (elect_one()) {
-                        const uint32_t v_at = ring_at + slot * kBlock;
+                        // d = 64: the second 64 rows of M are the first again (a stride of 0)
+                        const uint64_t v_at = tc::desc_mnmajor_sw128(ring_at + slot * G::kSlot, G::kPer == 2 ? kBlock : 0);
 #pragma unroll
                         for (int i = 0; i < 2 * kTile / 16; ++i)   // the leading term of P, then the other
-                            // d = 64: the second 64 rows of M are the first again (a stride of 0)
-                            tc::mma_bf16_ss(tm + G::kO + mb * (64 * NB), tc::desc_mnmajor_sw128(v_at + (i & 7) * 2048, per == 2 ? kBlock : 0),
-                                            tc::desc_mnmajor_sw128(ring_at + kPOff + (i >> 3) * G::kP + (i & 7) * 2048, kBlock), id_o,
-                                            j > 0 || i > 0);
+                            tc::mma_bf16_ss(tm + G::kO + mb * (64 * NB), v_at + (i & 7) * 2048 / 16, p_at + ((i >> 3) * G::kP + (i & 7) * 2048) / 16,
+                                            id_o, j > 0 || i > 0);
                         tc::mma_commit(&bars.kv_empty[slot]);
-                        if (per == 2) tc::mma_commit(&bars.kv_empty[slot + per - 1]);
                         if (mb == G::kMb - 1) {
-                            tc::mma_commit(&bars.pv_done);
-                            mbar_arrive(&bars.pv_done);
+                            tc::mma_commit(&bars.pv_done[(g + j) & 1]);
+                            mbar_arrive(&bars.pv_done[(g + j) & 1]);
                         }
                     }
                     __syncwarp();
-                    slot += per;
-                    if (slot == G::kSlots) slot = 0, phase ^= 1;
+                    if (++slot == G::kSlots) slot = 0, phase ^= 1;
                 }
                 if (!fine) break;
             }
@@ -586,7 +594,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- queries, and values at the ends
-        uint32_t items = 0, block0 = 0, looked = 0;              // block0: the item's first block of the ring
+        uint32_t items = 0, slot0 = 0, looked = 0;               // slot0: the item's first slot of the ring
         bool fine = true;
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
@@ -610,11 +618,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 const int pos = first + j * kTile;
                 if (!see.partial(pos, kTile)) continue;
                 if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, &s_lost)))) break;
-                const uint32_t block = block0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kKb;   // V's first block
+                const uint32_t v_slot = slot0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kMb;   // V's first
                 for (int i = lane; i < kTile * G::kCpr; i += 32) {
                     const int r = i / G::kCpr, ch = i - r * G::kCpr;
                     if (pos + r <= see.p_min && pos + r >= see.lo_max) continue;
-                    uint4* q = reinterpret_cast<uint4*>(ring + (block + (ch >> 3)) % G::kSlots * kBlock + tile_chunk(kTile, r, ch & 7));
+                    uint4* q = reinterpret_cast<uint4*>(ring + (v_slot + ch / (8 * G::kPer)) % G::kSlots * G::kSlot + tile_chunk(kTile, r, ch % (8 * G::kPer)));
                     uint4 y = *q;
                     if (!(not_numbers(y.x) | not_numbers(y.y) | not_numbers(y.z) | not_numbers(y.w))) continue;
                     s_not_numbers = 1;
@@ -628,7 +636,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 __syncwarp();
                 if (lane == 0) set_count(&s_looked, looked);
             }
-            block0 += 2 * n * G::kKb;
+            slot0 += 2 * n * G::kMb;
         }
     }
     tc::fence_before_sync();
