@@ -670,9 +670,15 @@ cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
 }  // namespace
 
 bool tc_applies(const AttnArgs& a) {
-    const int64_t most = ((int64_t)1 << 39) - 1;      // elements: strides of a tensor map are below 2^40 bytes
-    return a.bf16 && a.Hq / a.Hk * a.T > 16 && a.cache.page % 8 == 0 && a.cache.page_stride <= most &&
-           a.cache.slot_stride <= most && a.cache.head_stride <= most;
+    // TMA copies whole 1024-byte atoms of eight slots, and strides below 2^40 bytes.
+    const int64_t most = ((int64_t)1 << 39) - 1;
+    if (!a.bf16 || a.cache.page % 8 != 0 || a.cache.page_stride > most || a.cache.slot_stride > most || a.cache.head_stride > most)
+        return false;
+    const int rows = a.Hq / a.Hk * a.T;
+    const int64_t elements = (int64_t)a.B * a.Hk * a.max_pages * a.cache.page * a.d;   // of K that the tables can hold
+    if (a.d == 64) return rows > 32 && elements >= 1 << 21;
+    if (a.d == 128) return rows > 16 && elements >= 1 << 21;
+    return elements >= (rows > 16 ? 1 << 22 : 1 << 23);
 }
 
 Plan plan_tc(int sms, int rows) {

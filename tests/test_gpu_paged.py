@@ -19,6 +19,7 @@ import numpy as np
 import pytest
 import torch
 
+from gdn_helpers import launched_kernels
 from oracle import paged
 
 pytestmark = pytest.mark.gpu
@@ -237,6 +238,19 @@ def test_append_far_into_a_large_pool(gdn):
 
 # ------------------------------------------------------------------------------ the attention
 
+# The kernel goes by what the block tables can hold. Every test of it runs with tables as wide as
+# its lengths (the streaming kernel), and with tables so wide that the tensor-memory kernel takes what it can.
+WIDE = False
+
+
+@pytest.fixture(params=["narrow", "wide"])
+def tables(request):
+    global WIDE
+    WIDE = request.param == "wide"
+    yield request.param
+    WIDE = False
+
+
 def _cache(g, pages, page, Hk, d, dt, layout="tokens"):
     r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dt)  # noqa: E731
     if layout == "tokens":
@@ -253,6 +267,8 @@ def _attn_case(T, Hq, Hk, d, dt, page, lens, q_len=None, layout="tokens", seed=0
     g = torch.Generator(device="cuda").manual_seed(seed)
     n = [-(-max(0, x) // page) for x in lens]
     width = max(1, max(n) + extra)
+    if WIDE:
+        width = max(width, (1 << 23) // (B * Hk * d * page) + 1)
     ids = np.random.default_rng(seed).permutation(sum(n) + 2)
     kc, vc = _cache(g, sum(n) + 2, page, Hk, d, dt, layout)
     table = np.full((B, width), -1, np.int32)
@@ -302,7 +318,7 @@ def _run_attn(gdn, x, window=0, scale=None, out_dtype=None, status=0, workspace=
 @pytest.mark.parametrize("T,Hq,Hk,d", [(1, 4, 4, 64), (1, 8, 1, 128), (1, 16, 1, 256), (2, 6, 2, 64), (8, 24, 4, 256), (8, 6, 1, 128),
                                        (16, 8, 1, 64), (16, 32, 2, 128), (3, 40, 1, 64), (16, 40, 1, 128), (5, 3, 3, 256), (11, 8, 4, 128)])
 @pytest.mark.parametrize("dt", [BF, F32])
-def test_attention_heads(gdn, T, Hq, Hk, d, dt):
+def test_attention_heads(gdn, tables, T, Hq, Hk, d, dt):
     x = _attn_case(T, Hq, Hk, d, dt, 16, [T, 100, 257], seed=T + Hq + d)
     _run_attn(gdn, x)
 
@@ -311,14 +327,14 @@ def test_attention_heads(gdn, T, Hq, Hk, d, dt):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("page,layout", [(1, "tokens"), (7, "side"), (16, "heads"), (24, "tokens"), (64, "side"), (128, "heads"), (400, "tokens")])
-def test_attention_pages_and_lengths(gdn, T, d, dt, page, layout):
+def test_attention_pages_and_lengths(gdn, tables, T, d, dt, page, layout):
     lens = [0, 1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 300, 5]
     _run_attn(gdn, _attn_case(T, 4, 2, d, dt, page, lens, layout=layout, seed=page + T))
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("window", [1, 3, 64, 100, 1000])
-def test_attention_window(gdn, window, dt):
+def test_attention_window(gdn, tables, window, dt):
     lens = [0, 1, 5, 64, 100, 101, 163, 450]
     for T, Hq in ((1, 2), (6, 12)):
         _run_attn(gdn, _attn_case(T, Hq, 2, 128, dt, 16, lens, seed=window), window=window)
@@ -326,7 +342,7 @@ def test_attention_window(gdn, window, dt):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("T,Hq", [(4, 2), (8, 12), (16, 16)])
-def test_attention_short_blocks(gdn, T, Hq, dt):
+def test_attention_short_blocks(gdn, tables, T, Hq, dt):
     # rows behind a sequence's q_len stay as they were; a block longer than the sequence has rows
     # that see nothing
     lens, ql = [3, 40, 0, 200, 7, 9, 1], [T, 1, 2, 3, 0, min(4, T), T]
@@ -334,7 +350,7 @@ def test_attention_short_blocks(gdn, T, Hq, dt):
         _run_attn(gdn, _attn_case(T, Hq, 2, 64, dt, 16, lens, q_len=ql, seed=T), window=window)
 
 
-def test_attention_output_type_and_scale(gdn):
+def test_attention_output_type_and_scale(gdn, tables):
     x = _attn_case(8, 12, 2, 128, BF, 16, [50, 333], seed=1)
     _run_attn(gdn, x, out_dtype=F32, scale=0.03)
     _run_attn(gdn, x, out_dtype=F32, scale=0.0)
@@ -343,14 +359,14 @@ def test_attention_output_type_and_scale(gdn):
 
 
 @pytest.mark.parametrize("T,Hq,Hk,d,dt", [(1, 8, 2, 128, BF), (8, 24, 4, 256, BF), (8, 12, 2, 128, BF), (16, 8, 1, 64, BF), (1, 4, 2, 64, F32)])
-def test_attention_long(gdn, T, Hq, Hk, d, dt):
+def test_attention_long(gdn, tables, T, Hq, Hk, d, dt):
     # many pieces for one row: one long sequence, and one beside short ones
     _run_attn(gdn, _attn_case(T, Hq, Hk, d, dt, 64, [20011], seed=2))
     _run_attn(gdn, _attn_case(T, Hq, Hk, d, dt, 16, [5, 9000, 0, 64, 1], seed=2))
 
 
 @pytest.mark.parametrize("T,Hq", [(1, 3), (8, 12)])
-def test_attention_many_sequences(gdn, T, Hq):
+def test_attention_many_sequences(gdn, tables, T, Hq):
     rng = np.random.default_rng(T)
     _run_attn(gdn, _attn_case(T, Hq, 3, 64, BF, 16, rng.integers(0, 40, 700).tolist(), seed=T))
 
@@ -358,7 +374,7 @@ def test_attention_many_sequences(gdn, T, Hq):
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("T,Hq", [(4, 2), (8, 16)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_attention_unseen_infinities(gdn, T, Hq, dt, bad):
+def test_attention_unseen_infinities(gdn, tables, T, Hq, dt, bad):
     # the last draft's key and value are not numbers: the rows before it do not see them
     x = _attn_case(T, Hq, 2, 64, dt, 16, [70, T, 130], seed=4)
     clean = _run_attn(gdn, x)
@@ -380,7 +396,7 @@ def test_attention_unseen_infinities(gdn, T, Hq, dt, bad):
 
 
 @pytest.mark.parametrize("T,Hq", [(1, 4), (8, 16)])
-def test_attention_extreme_scores(gdn, T, Hq):
+def test_attention_extreme_scores(gdn, tables, T, Hq):
     # one key far ahead of all others, then all scores very negative, then equal
     x = _attn_case(T, Hq, 2, 128, BF, 16, [600], seed=6)
     x["kc"][x["table"][0, 20], 3] = x["q"][0, 0, 0] * 40
@@ -394,7 +410,7 @@ def test_attention_extreme_scores(gdn, T, Hq):
 
 
 @pytest.mark.parametrize("T,Hq,dt", [(1, 4, BF), (8, 16, BF), (2, 4, F32)])
-def test_attention_bad_lengths_and_pages(gdn, T, Hq, dt):
+def test_attention_bad_lengths_and_pages(gdn, tables, T, Hq, dt):
     x = _attn_case(T, Hq, 2, 64, dt, 16, [40, 50, 60, 70, 33], q_len=[T] * 5, seed=7)
     x["kv"][1], x["kv"][2] = -1, x["table"].shape[1] * 16 + 1
     x["ql"][3], x["ql"][4] = T + 1, -1
@@ -414,15 +430,16 @@ def test_attention_far_into_a_large_pool(gdn):
     pages = (1 << 31) // (page * Hk * d) + 3
     kc, vc = torch.empty(pages, page, Hk, d, dtype=BF, device="cuda"), torch.empty(pages, page, Hk, d, dtype=BF, device="cuda")
     kc[-2:], vc[-2:] = torch.randn(2, 2, page, Hk, d, device="cuda").to(BF)
-    table = np.array([[pages - 1, pages - 2]], np.int32)
-    for T, Hq in ((1, 16), (8, 48)):
+    for T, Hq, width in ((1, 16, 2), (8, 48, 2), (8, 48, 40)):
+        table = np.full((1, width), -1, np.int32)
+        table[0, :2] = pages - 1, pages - 2
         q = torch.randn(1, T, Hq, d, device="cuda").to(BF)
         o, lse = gdn.paged_attention(q, kc, vc, _i32(table), _i32([300]), lse=(l := torch.empty(1, T, Hq, device="cuda"))), l
         torch.cuda.synchronize()
         _check_attn(dict(q=q, kc=kc[-2:], vc=vc[-2:], table=np.array([[1, 0]]), kv=[300], ql=None), o, lse)
 
 
-def test_attention_streams_graphs_and_repeats(gdn):
+def test_attention_streams_graphs_and_repeats(gdn, tables):
     # the same bits from a side stream, from two captured graphs (a workspace each), and again
     cases = [_attn_case(8, 24, 4, 128, BF, 16, [3000, 17, 800], seed=9), _attn_case(1, 8, 4, 64, BF, 16, [900, 1, 64], seed=10)]
     want = [_run_attn(gdn, x) for x in cases]
@@ -454,6 +471,22 @@ def test_attention_streams_graphs_and_repeats(gdn):
     torch.cuda.synchronize()
     for (o, lse, _, _), (wo, wl) in zip(outs, want):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+def test_attention_kernel_choice(gdn):
+    # each branch of the rule, on both of its sides
+    def name(B, T, Hq, Hk, d, dt, page, capacity):
+        x = _attn_case(T, Hq, Hk, d, dt, page, [20] * B, extra=capacity // page - -(-20 // page), seed=1)
+        _, names = launched_kernels(lambda: _run_attn(gdn, x, check=False))
+        return any("attention_tc_kernel" in n for n in names)
+
+    assert not name(1, 8, 24, 4, 64, BF, 16, 4096) and name(1, 8, 24, 4, 64, BF, 16, 8192)
+    assert not name(8, 4, 32, 4, 64, BF, 16, 8192) and name(8, 5, 32, 4, 64, BF, 16, 8192)
+    assert not name(1, 8, 24, 4, 128, BF, 16, 2048) and name(1, 8, 24, 4, 128, BF, 16, 4096)
+    assert not name(8, 2, 32, 4, 128, BF, 16, 4096) and name(8, 3, 32, 4, 128, BF, 16, 4096)
+    assert not name(1, 8, 24, 4, 256, BF, 16, 2048) and name(1, 8, 24, 4, 256, BF, 16, 4096)
+    assert not name(1, 1, 24, 4, 256, BF, 16, 4096) and name(1, 1, 24, 4, 256, BF, 16, 8192)
+    assert not name(8, 8, 24, 4, 128, F32, 16, 8192) and not name(8, 8, 24, 4, 128, BF, 20, 8200)
 
 
 def test_attention_empty_batch(gdn):
