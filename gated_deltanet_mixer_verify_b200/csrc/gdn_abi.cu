@@ -930,7 +930,7 @@ gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t w
     a.Hk = shape->H_kv;
     a.d = shape->d;
     a.max_pages = shape->max_pages;
-    a.window = window;
+    a.window = window > (1 << 30) ? 0 : window;      // no sequence is longer than 2^30
     a.bf16 = shape->dtype == GDN_BF16;
     a.out_bf16 = shape->out_dtype == GDN_BF16;
     a.scale = scale;

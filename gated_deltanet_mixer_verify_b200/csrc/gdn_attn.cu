@@ -13,7 +13,7 @@
 // Precision. bf16 products are exact in fp32. The weights 2^(s - m) enter the second product as two
 // bf16 terms (2^-17 relative), because one (2^-9) would be as large as the rounding of a bf16
 // result; the matrix units have the room. fp32 operands are split into two tf32 terms each, and the
-// three products that matter are added (2^-21). Statistics and sums are fp32.
+// three products that matter are added (2^-22). Statistics and sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -72,9 +72,11 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo with hi the leading 11 bits; lo's own tail (2^-22 of x) is left to the matrix unit.
+// x = hi + lo exactly, hi rounded to the 11 bits of tf32 (half away from zero), lo (12 bits at most) left to
+// the matrix unit, which drops what is below its 11 bits: 2^-23 of x. Cutting instead of rounding would lose
+// four times that, always towards zero.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {

@@ -524,7 +524,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  *              calls that may overlap on the GPU need one each (two captured graphs included).
  * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products
  * with v as two bf16 terms (2^-17 relative). fp32 products are formed from split tf32 terms
- * (about 2^-21). The result does not depend on the order in which CTAs finish.
+ * (about 2^-22; finite values above 2^127 (2 - 2^-12) count as infinite). The result does not depend on the order in which CTAs finish.
  * shape: B 0..65535, T 1..16, d 64, 128 or 256, H_q <= 65535.
  */
 gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,

@@ -128,6 +128,14 @@ def test_plan_counts_that_cannot_be(gdn):
     assert ref["status"] == 1 | 4 | 16
 
 
+def test_plan_free_count_that_cannot_be(gdn):
+    # a count outside the pool counts as an empty or a full list
+    for count, want in ((-3, 0), (99, 7)):
+        st, c = _status(), _i32([count])
+        gdn.kv_plan(_i32([0]), _i32([0]), _i32([[-1] * 4]), _i32(range(7)), c, 2, 16, add_len=_i32([0]), status_word=st)
+        assert int(st) == 4 and int(c) == want
+
+
 def test_plan_empty_batch_and_zero_adds(gdn):
     e = lambda *sh, dt=torch.int32: torch.empty(sh, dtype=dt, device="cuda")  # noqa: E731
     count = _i32([5])
@@ -354,6 +362,9 @@ def test_attention_output_type_and_scale(gdn, tables):
     x = _attn_case(8, 12, 2, 128, BF, 16, [50, 333], seed=1)
     _run_attn(gdn, x, out_dtype=F32, scale=0.03)
     _run_attn(gdn, x, out_dtype=F32, scale=0.0)
+    _run_attn(gdn, x, scale=-0.06)
+    for window in (1 << 30, (1 << 31) - 1):
+        _run_attn(gdn, x, window=window)
     y = _attn_case(1, 12, 2, 128, F32, 16, [50, 333], seed=1)
     _run_attn(gdn, y, out_dtype=BF)
 
