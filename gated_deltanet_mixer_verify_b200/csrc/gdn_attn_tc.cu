@@ -44,7 +44,9 @@ namespace {
 using namespace dev;
 
 constexpr int kTile = 128;                      // positions per tile, and per unit
-constexpr int kExtra = 2;                       // units that an item costs besides (its first and last steps overlap nothing)
+// Units that an item costs besides (its first and last steps overlap little). Measured with 2, 3, 4, us: one sequence of
+// 32K positions (d 256, 48 rows) 52.3, 45.8, 47.5; 32 sequences of 100 .. 8192 117.9, 113.5, 112.9; 128 of 100 .. 512 97.7, 96.5, 96.2.
+constexpr int kExtra = 3;
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
@@ -86,9 +88,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// The bits of those of two bf16 values that are infinite or NaN.
-__device__ __forceinline__ uint32_t not_numbers(uint32_t w) {
-    return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+// Two bf16 values, with zeros for those that are infinite or NaN.
+__device__ __forceinline__ uint32_t numbers(uint32_t w) {
+    return w & ~(((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u));
+}
+// 0 w + sum, which is NaN from the first w that is infinite or NaN on.
+__device__ __forceinline__ __nv_bfloat162 taint(uint32_t w, __nv_bfloat162 sum) {
+    return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(0.f, 0.f), sum);
 }
 
 // Waits of a whole warp, its lanes agreeing, that give up when the CTA has been given up, or after
@@ -239,17 +245,21 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         const float cs = x.c == 0.f ? 1.f : fabsf(x.c);
         // the product of tile t is done
         auto product_done = [&](uint32_t t) { return await_warp(&bars.pv_done[t & 1], (t >> 1) & 1, &s_lost); };
-        uint32_t g = 0;                                          // tiles done by this CTA
+        // Tiles done by this CTA. Its first item begins with a tile -1, worked without waiting for anything and
+        // forgotten: while the first keys are on their way, it brings the instructions in (4,000 cycles of misses).
+        uint32_t g = ~0u;
         bool fine = true;
         float l[32];
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
+            for (int j = g == ~0u ? -1 : 0; j < n; ++j, ++g) {
+                if (j <= 0) {
 #pragma unroll
-            for (int r = 0; r < 32; ++r) l[r] = 0.f;
-            for (int j = 0; j < n; ++j, ++g) {
-                if (!(fine = await_warp(&bars.s_full[g & 1], (g >> 1) & 1, &s_lost))) break;
+                    for (int r = 0; r < 32; ++r) l[r] = 0.f;
+                }
+                if (j >= 0 && !(fine = await_warp(&bars.s_full[g & 1], (g >> 1) & 1, &s_lost))) break;
                 tc::fence_after_sync();
                 float s[32];
                 if (chunks > 0) {
@@ -270,7 +280,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         for (int r = 0; r < 32; ++r)
                             if (r < f || r >= e) s[r] = -INFINITY;
                     }
-                    bool move = j == 0;
+                    bool move = j <= 0;
                     if (j > 0) {
                         float over = -INFINITY;
 #pragma unroll
@@ -346,7 +356,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[g & 1]);
+                if (lane == 0 && j >= 0) mbar_arrive(&bars.p_full[g & 1]);
             }
             if (!fine) break;
             // the sums, and where the rows go
@@ -594,48 +604,79 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- queries, and values at the ends
+        constexpr int kAtOnce = 8;                               // reads of values in flight, 16 bytes each
+        constexpr int kQRows = 32 / G::kCpr;                     // rows of Q that the warp asks for at once
         uint32_t items = 0, slot0 = 0, looked = 0;               // slot0: the item's first slot of the ring
         bool fine = true;
-        while (fine && w.next(x)) {
-            if (row0 / share >= w.s.rows) continue;
-            const Sight see(a, w.s, row0, row0 + rows, share);
-            const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
-            if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, &s_lost))) break;
-            for (int i = lane; i < rows * G::kCpr; i += 32) {
-                const int r = i / G::kCpr, ch = i - r * G::kCpr, row = row0 + r, t = row / share;
-                const int64_t qr = ((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + (row - t * share);
-                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), static_cast<const __nv_bfloat16*>(a.q) + qr * D + ch * 8);
+        // The next item and its queries, when the last product with the former item's has been made.
+        auto next_item = [&]() -> bool {
+            do {
+                if (!w.next(x)) return false;
+            } while (row0 / share >= w.s.rows);
+            if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, &s_lost))) return false;
+            const int ch = lane % G::kCpr;
+            int r = lane / G::kCpr, t = (row0 + r) / share, head = row0 + r - t * share;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + head) * D + ch * 8;
+#pragma unroll 4
+            for (; r < rows; r += kQRows) {
+                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), q);
+                q += kQRows * D;
+                for (head += kQRows; head >= share; head -= share) q += (int64_t)(a.Hq - share) * D;   // the next token's
             }
             cp_async_wait_all();
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_full);
             ++items;
+            return true;
+        };
+        bool more = next_item();
+        while (more) {
+            const int kv = w.s.kv, n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
+            const Sight see(a, w.s, row0, row0 + rows, share);
             // Values that are not numbers, at positions that some row does not see, would reach that row
             // as 0 times infinity. They leave a zero in the tile; the rows that do see them get them at
-            // the end (`repair` above).
-            for (int j = 0; j < n; ++j) {
+            // the end (`repair` above). The last tile comes after the next item's queries, which it would keep
+            // waiting: its scores, the last of this item, are formed by then.
+            for (int j = 0; j < n && fine; ++j) {
+                if (j == n - 1) more = next_item();
                 const int pos = first + j * kTile;
-                if (!see.partial(pos, kTile)) continue;
+                if (!fine || !see.partial(pos, kTile)) continue;
                 if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, &s_lost)))) break;
                 const uint32_t v_slot = slot0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kMb;   // V's first
-                for (int i = lane; i < kTile * G::kCpr; i += 32) {
-                    const int r = i / G::kCpr, ch = i - r * G::kCpr;
-                    if (pos + r <= see.p_min && pos + r >= see.lo_max) continue;
-                    uint4* q = reinterpret_cast<uint4*>(ring + (v_slot + ch / (8 * G::kPer)) % G::kSlots * G::kSlot + tile_chunk(kTile, r, ch % (8 * G::kPer)));
-                    uint4 y = *q;
-                    if (!(not_numbers(y.x) | not_numbers(y.y) | not_numbers(y.z) | not_numbers(y.w))) continue;
-                    s_not_numbers = 1;
-                    y.x &= ~not_numbers(y.x);
-                    y.y &= ~not_numbers(y.y);
-                    y.z &= ~not_numbers(y.z);
-                    y.w &= ~not_numbers(y.w);
-                    *q = y;
+                // rows 0 .. low - 1 and high .. stop - 1 of the tile; behind them TMA has left zeros
+                const int stop = min(kTile, (max(kv - pos, 0) + run - 1) / run * run);
+                const int low = min(max(see.lo_max - pos, 0), stop), high = min(max(see.p_min + 1 - pos, low), stop);
+                const int ch = lane % G::kCpr, r_lane = lane / G::kCpr;
+                unsigned char* const v_at = ring + (v_slot + ch / (8 * G::kPer)) % G::kSlots * G::kSlot;
+                for (int r0 = 0; r0 < stop; r0 += kAtOnce * kQRows) {
+                    if (r0 >= low && r0 + kAtOnce * kQRows <= high) continue;
+                    uint4 y[kAtOnce];
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e)            // up to 32 rows: all of the tile, if not of the rows before stop
+                        y[e] = *reinterpret_cast<const uint4*>(v_at + tile_chunk(kTile, r0 + r_lane + e * kQRows, ch % (8 * G::kPer)));
+                    __nv_bfloat162 sum[2] = {__floats2bfloat162_rn(0.f, 0.f), __floats2bfloat162_rn(0.f, 0.f)};
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e) {
+                        sum[0] = taint(y[e].y, taint(y[e].x, sum[0]));
+                        sum[1] = taint(y[e].w, taint(y[e].z, sum[1]));
+                    }
+                    const __nv_bfloat162 both = __hadd2(sum[0], sum[1]);
+                    if (__low2float(both) == 0.f && __high2float(both) == 0.f) continue;
+#pragma unroll
+                    for (int e = 0; e < kAtOnce; ++e) {
+                        const int r = r0 + r_lane + e * kQRows;
+                        const uint4 z = make_uint4(numbers(y[e].x), numbers(y[e].y), numbers(y[e].z), numbers(y[e].w));
+                        if ((r >= low && r < high) || (z.x == y[e].x && z.y == y[e].y && z.z == y[e].z && z.w == y[e].w)) continue;
+                        s_not_numbers = 1;
+                        *reinterpret_cast<uint4*>(v_at + tile_chunk(kTile, r, ch % (8 * G::kPer))) = z;
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) set_count(&s_looked, looked);
             }
+            if (!fine) break;
             slot0 += 2 * n * G::kMb;
         }
     }
