@@ -10,10 +10,10 @@ namespace attn {
 // 16 rows each, and read the cache once per 16, 32 for d <= 128) and for little work (its CTAs start sooner, two or
 // three to an SM). What the lengths are is not known on the host; the tables' capacity stands for them. Measured, streaming
 // against this kernel, us (4 key heads; B x positions, rows):
-//   d 64:  1 x 8192, 48: 20.0, 19.9; 32 x 4096, 32: 60, 61; 32 x 4096, 48: 93, 63; 128 x 512, 48: 75, 85
-//   d 128: 1 x 2048, 48: 17.0, 18.6; 1 x 4096, 48: 19.6, 19.2; 32 x 4096, 16: 59, 62; 32 x 4096, 32: 90, 69; 32 x 4096, 48: 150, 74
-//   d 256: 1 x 2048, 48: 19.7, 24.6; 1 x 4096, 64: 28.4, 26.3; 1 x 4096, 16: 16.7, 18.4; 1 x 8192, 16: 20.4, 20.4;
-//          32 x 4096, 8: 128, 104; 32 x 4096, 48: 346, 118
+//   d 64:  1 x 8192, 48: 19.8, 19.6; 32 x 4096, 32: 60, 62; 32 x 4096, 48: 94, 64; 128 x 512, 48: 77, 75
+//   d 128: 1 x 2048, 48: 17.0, 17.2; 1 x 4096, 48: 19.1, 17.9; 32 x 4096, 16: 59, 65; 32 x 4096, 24: 87, 69; 32 x 4096, 48: 148, 74
+//   d 256: 1 x 2048, 48: 19.5, 20.6; 1 x 4096, 48: 24.3, 21.3; 1 x 4096, 16: 17.7, 19.1; 1 x 8192, 16: 24.5, 23.0;
+//          32 x 512, 8: 32.5, 30.1; 32 x 4096, 8: 128, 106; 32 x 4096, 48: 346, 119
 bool tc_applies(const AttnArgs& a);
 // Its layout for `rows` rows per key head on `sms` SMs, and its launch.
 Plan plan_tc(int sms, int rows);

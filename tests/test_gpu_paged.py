@@ -217,6 +217,12 @@ def test_append_layouts(gdn, B, T, Hq, Hk, page, layout, fused, in_place, text, 
             text=text, seed=B + T)
 
 
+@pytest.mark.parametrize("B,T,Hq,Hk,d", [(3, 2100, 2, 1, 64), (1, 6151, 9, 3, 128)])
+def test_append_prompts(gdn, B, T, Hq, Hk, d):
+    # so many tokens that a CTA takes sixteen of them, and the last CTA fewer
+    _append(gdn, B, T, Hq, Hk, d, 16, [8], BF, seed=d)
+
+
 def test_append_far_positions(gdn):
     # angles of up to 2^31 radians: what is left of a turn would be gone in 32 bits
     _append(gdn, 2, 64, 2, 1, 64, 64, [32], F32, far=(1 << 31) - 1, norm=False, seed=3)
@@ -404,6 +410,32 @@ def test_attention_unseen_infinities(gdn, tables, T, Hq, dt, bad):
     o, _ = _run_attn(gdn, x, window=20, check=False)
     assert torch.equal(o[:, 1:], clean[0][:, 1:])
     assert not bool(torch.isfinite(o[:, 0, :, 1]).any()) and torch.equal(o[:, 0, :, 2:], clean[0][:, 0, :, 2:])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 48])
+def test_attention_unseen_values_by_place(gdn, tables, d, page):
+    # a value that only the last row sees and one that only the first row sees, in any column of any tile
+    T, W = 8, 150
+    rng = np.random.default_rng(d + page)
+    x = _attn_case(T, 12, 2, d, BF, page, [T, 128, 136, 260, 300, 517, 640], seed=d)
+    clean = _run_attn(gdn, x, window=W)
+    expect = clean[0].clone()
+    for b, n in enumerate(x["kv"]):
+        for pos, row in ((n - 1, T - 1), (n - T - W + 1, 0)):
+            if pos < 0:
+                continue
+            h, col = int(rng.integers(2)), int(rng.integers(d))
+            x["vc"][x["table"][b, pos // page], pos % page, h, col] = float("inf")
+            expect[b, row, 6 * h:6 * h + 6, col] = float("inf")
+    o, _ = _run_attn(gdn, x, window=W, check=False)
+    assert torch.equal(o, expect)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_attention_many_items_for_each_cta(gdn, tables, d):
+    rng = np.random.default_rng(d)
+    _run_attn(gdn, _attn_case(8, 12, 2, d, BF, 8, rng.integers(0, 400, 260).tolist(), seed=d))
 
 
 @pytest.mark.parametrize("T,Hq", [(1, 4), (8, 16)])
