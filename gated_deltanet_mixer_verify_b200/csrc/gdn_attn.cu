@@ -10,6 +10,14 @@
 //   s = q k^T (base-2 exponents), running maximum m and sum l per row, o = o 2^(m - m') + 2^(s - m') v.
 // A warp's maxima, totals and sums are joined with the other warps' when the CTA leaves the item.
 //
+// Bound: HBM. Measured, bf16, one row per sequence: 64 sequences of 500 .. 16,384 positions, 32 heads over 8, d 128
+// (2.2 GB) 352 us, 96% of the measured copy rate; 128 sequences of 1 .. 2048, 16 heads over 16 (1.07 GB) 193 us,
+// 85% (2,048 short items: their beginnings and ends); one sequence of 1,024 12 us, latency: the page numbers, the
+// values and the join one after another. fp32 (three products for one, 16 sequences, window 1000) 20 us, latency too.
+// One wave of CTAs, because more cost: two, three, four waves 354, 361, 367 and 197, 203, 209 us. An item counts
+// as three units more: with 2, 3, 5, 7 the second case took 208, 193, 188, 193 us, all others the same within 2%
+// but 32 sequences of 100 .. 2048 (d 128) 27.0, 26.1, 26.7, 28.1.
+//
 // Precision. bf16 products are exact in fp32. The weights 2^(s - m) enter the second product as two
 // bf16 terms (2^-17 relative), because one (2^-9) would be as large as the rounding of a bf16
 // result; the matrix units have the room. fp32 operands are split into two tf32 terms each, and the

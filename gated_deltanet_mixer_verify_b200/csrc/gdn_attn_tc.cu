@@ -15,19 +15,25 @@
 // bf16 have the range; nothing is lost below it), which is when maxima are taken again and O rescaled.
 // The sums of the weights stay with the threads until the item ends.
 //
-// One CTA per SM with roles for its warps: softmax and outputs (four warps for each 32 rows), one that
-// fetches keys and values into a ring of [128 positions][64 columns] blocks by TMA (one copy per run
+// One CTA per SM with roles for its warps: softmax and outputs (four warps for each 32 rows), two that
+// fetch keys and values into a ring of [128 positions][64 columns] blocks by TMA (one copy per run
 // of a page's slots, so pages of any multiple of 8 slots and any strides will do), one that issues
 // the products, one that fetches queries and looks over the values at the ends of what the rows see.
 // The order of products, and of the ring, is K 0, K 1, V 0, K 2, V 1, ...: scores of the next tile
 // are formed before the values of this one are needed, so a block is used up as it lands, the
 // softmax runs while values land, and the whole ring is copies in flight. Every wait is bounded.
 //
-// Measured on the way (one sequence, 32K positions, 8 rows x 6 heads, d 256; 134 MB): rows as M, one thread
-// per row, P in tensor memory, 71 us; positions as M with the steps of a tile one after the other
-// (7,300 cycles per tile of 128, of which HBM needs 5,680), 68 us. A product of M 128, N 48, K 16
-// takes 48 cycles, bound by its reads of A from shared memory, and waits on barriers take 200 while
-// products run, so single steps cannot be made short; they are overlapped instead.
+// Bound: HBM and the chain within a tile together. A tile of 128 positions (d 256) is 128 KB, 5,700 cycles of
+// an SM's share of HBM; its 16 score and 32 output products of M 128, N 48, K 16 take 2,300 (48 each,
+// bound by their reads of A from shared memory). In the steady state a tile takes 4,900 cycles where all
+// SMs hold the same number of them; beside it stand the first tiles (the pages' numbers, keys, scores and values
+// one after another: 20 us cold) and the ends of items (the maxima anew, the look, the output: 2 tiles).
+// Measured: one sequence of 32K positions, 8 rows x 6 heads, d 256 (134 MB) 46 us; 32 of 100 .. 8192 (546 MB)
+// 113 to 118 us, 4.7 TB/s, 72% of the measured copy rate.
+// Steps, the first of these cases, us: rows as M, one thread per row, P in tensor memory 71; positions as M with the
+// steps of a tile one after the other 68; overlapped, and the join's grid small 56; programmatic dependents 51 to 54;
+// the look in rows at once, the next queries before the last look, items weighted 3 46.
+// Not faster: fetching with cp.async (5,600 to 9,800 cycles a tile; the proxy fence waits for copies in flight).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -515,7 +521,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         // The whole warp walks and waits alike and one elected lane issues: what the products take (addresses,
         // descriptors) is then the same in every lane by construction, and a run of products differs by
         // constants only: 48 cycles each, where descriptors made one by one, or in a lane's own branch, cost
-        // 80 to 140. A wait costs 150 more, so there is one for each slot.
+        // 80 to 140. A wait costs 150 more, so there is one for each slot of the ring.
         const uint32_t tm = __shfl_sync(kFull, tmem, 0);
         const uint32_t N = (uint32_t)(rows + 15) / 16 * 16;
         const uint32_t id_s = tc::idesc_bf16(kTile, N, false), id_o = tc::idesc_bf16(128, N, true);

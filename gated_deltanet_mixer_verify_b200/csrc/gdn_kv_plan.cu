@@ -5,7 +5,8 @@
 // Whole numbers only: two prefix sums over the sequences (pages returned, pages needed) place
 // every sequence's pages on the free list, so the result does not depend on any order of
 // execution. One CTA does it, a thread for each sequence, because every step hangs on the sums; it is a chain
-// of six dependent reads, bound by their latency. The slots of a block of a few tokens are formed there
+// of six dependent reads, bound by their latency: 3 us on the device for one sequence, 7.4 us for 256 of a block of 8
+// (11.7 us under a profiler, cold), 13 us and 3 for the slots of 32 prompts of up to 8192. The slots of a block of a few tokens are formed there
 // too; those of prompts (one each for tens of thousands of tokens) by a second kernel over all SMs,
 // launched as a programmatic dependent.
 #include <cuda_runtime.h>

@@ -4,7 +4,7 @@
 // Every element of q, k and v is read once and written once; the angles of a token (rot / 2 of
 // them) are the same for all its heads, so a CTA forms them once in shared memory: the product
 // position x frequency in fp64, reduced to a fraction of a turn there, cosine and sine in fp32.
-// Measured for 24,576 tokens of 48 heads, d 128, bf16, head norms, three axes (604 MB): 144 us, 64% of
+// Measured for 24,576 tokens of 48 heads, d 128, bf16, head norms, three axes (604 MB): 142 us, 65% of
 // the measured copy rate; the same kernel without its arithmetic takes 109 us, without the norm 128 us, without
 // the cosines no less; with 8 tokens per CTA 151 us, with 4 167 us, with 32 169 us. So it is bound by issue and HBM together. A block of a few tokens (8 x 32
 // heads, d 256) takes 3.5 us, launch and three dependent reads.
