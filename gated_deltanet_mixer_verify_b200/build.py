@@ -4,13 +4,15 @@
 
 Each csrc/*.cu file is compiled by nvcc (in parallel) and linked into the package
 directory, next to this file, with the CUDA runtime linked statically so that the
-library loads on machines without a GPU.
+library loads on machines without a GPU. _binding.so beside it (csrc/binding.cpp, by the host
+compiler, against PyTorch's headers) is the native half of gdn.py's argument checks.
 """
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -51,8 +56,29 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so if its source is newer than it; return its path."""
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(
+            os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.abspath(__file__))):
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on %s:\n%s%s" % (CXX, BINDING_SRC, r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgdn.so if any source is newer than it; return its path."""
+    """Compile and link libgdn.so (and _binding.so) if any source is newer than it; return its path."""
+    build_binding(force)
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -112,6 +112,22 @@ def _load():
     return lib
 
 
+_native_module = None
+
+
+def _native():
+    """The native half of the argument checks (csrc/binding.cpp)."""
+    global _native_module
+    if _native_module is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("_binding.so not built: run `python -m gated_deltanet_mixer_verify_b200.build` "
+                              "(or __graft_entry__.build())") from e
+        _native_module = _binding
+    return _native_module
+
+
 def lib():
     """The loaded ctypes library (raises ImportError if it was never built)."""
     return _load()
@@ -490,9 +506,7 @@ _pack_rope = struct.Struct("=8if4x4q").pack
 
 
 def _want(name, t, dt, shape, dev):
-    """Device pointer of a contiguous tensor of one type and shape on device ``dev``; None stays None.
-    (Straight-line checks: these calls take up to fourteen tensors, and small ones are over in
-    a few microseconds.)"""
+    """Device pointer of a contiguous tensor of one type and shape on device ``dev``; None stays None."""
     if t is None:
         return None
     if t.dtype is not dt:
@@ -506,11 +520,18 @@ def _want(name, t, dt, shape, dev):
     return t.data_ptr()
 
 
+def _pointers(spec, dev, dims, *tensors):
+    """Device pointers of a call's contiguous tensors. ``spec``: (name, dtype, axes) of each, axis i with dims[i]
+    entries. All are looked at in one native call, and one by one where that finds something wrong."""
+    return _native().pointers(spec, dev, dims, *tensors) or tuple(
+        [_want(name, t, dt, tuple([dims[i] for i in axes]), dev) for (name, dt, axes), t in zip(spec, tensors)])
+
+
 def _raw_stream(stream, dev) -> int:
     """The stream to launch on, after the last check of the tensors' common device."""
     if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()                  # a CUDA tensor exists, so CUDA is up
     if dev != cur:
         raise ValueError("tensor is on cuda:%d but the current CUDA device is cuda:%d; call under "
                          "torch.cuda.device(%d)" % (dev, cur, dev))
@@ -529,7 +550,10 @@ def _token_stride(name, t, B, T, H, d) -> int:
 
 
 def _cache(k_cache, v_cache, H_kv, d, dtype, dev):
-    """(page size, pages, strides) of the caches."""
+    """(page size, pages, page, slot and head stride, k's and v's pointer) of the caches."""
+    found = _native().caches(k_cache, v_cache, dtype, dev, H_kv, d)
+    if found is not None:
+        return found
     shape = k_cache.shape
     if len(shape) != 4 or shape != v_cache.shape or shape[2] != H_kv or shape[3] != d:
         raise ValueError("k_cache and v_cache must be [pages, page_size, %d, %d]" % (H_kv, d))
@@ -542,7 +566,19 @@ def _cache(k_cache, v_cache, H_kv, d, dtype, dev):
         raise ValueError("the caches' last axis must be contiguous")
     if k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise ValueError("the caches are not where q is")
-    return shape[1], shape[0], strides
+    return (shape[1], shape[0], *strides[:3], k_cache.data_ptr(), v_cache.data_ptr())
+
+
+# (name, type, axes) of the tensors of a call
+_PLAN = tuple((name, _I32, axes) for name, axes in
+              (("seq_len", (0,)), ("seq_len_out", (0,)), ("commit_len", (0,)), ("block_len", (0,)), ("add_len", (0,)),
+               ("n_pages", (0,)), ("n_pages_out", (0,)), ("block_table", (0, 1)), ("free_list", (2,)), ("free_count", (4,)),
+               ("free_count_out", (4,)), ("kv_len", (0,)), ("q_len", (0,)))) + (("slot_map", _I64, (0, 3)), ("status_word", _I32, (4,)))
+_APPEND = (("inv_freq", _F32, (2,)), ("positions", _I32, (3, 0, 1)), ("kv_len", _I32, (0,)), ("q_len", _I32, (0,)),
+           ("slot_map", _I64, (0, 1)), ("q_norm", _F32, (4,)), ("k_norm", _F32, (4,)), ("status_word", _I32, (5,)))
+_ATTENTION = {(dt, odt): (("q", dt, (0, 1, 2, 3)), ("block_table", _I32, (0, 4)), ("kv_len", _I32, (0,)), ("q_len", _I32, (0,)),
+                          ("o", odt, (0, 1, 2, 3)), ("lse", _F32, (0, 1, 2)), ("status_word", _I32, (5,)))
+              for dt in (torch.float32, torch.bfloat16) for odt in (torch.float32, torch.bfloat16)}
 
 
 def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, commit_len=None, add_len=None,
@@ -556,8 +592,8 @@ def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, 
     int32, slot_map [B, T] int64)."""
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and free_list [pages]")
-    B, max_pages = table_shape = block_table.shape
-    pages = free_list.shape
+    B, max_pages = block_table.shape
+    pages = free_list.shape[0]
     dev = block_table.get_device()
     if kv_len is None:
         kv_len = torch.empty(B, dtype=_I32, device=block_table.device)
@@ -565,20 +601,11 @@ def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, 
         q_len = torch.empty(B, dtype=_I32, device=block_table.device)
     if slot_map is None:
         slot_map = torch.empty((B, T), dtype=_I64, device=block_table.device)
-    per, one = (B,), (1,)
-    p_seq = _want("seq_len", seq_len, _I32, per, dev)
-    p_held = _want("n_pages", n_pages, _I32, per, dev)
-    p_count = _want("free_count", free_count, _I32, one, dev)
-    args = (p_seq, p_seq if seq_len_out is None else _want("seq_len_out", seq_len_out, _I32, per, dev),
-            _want("commit_len", commit_len, _I32, per, dev), _want("block_len", block_len, _I32, per, dev),
-            _want("add_len", add_len, _I32, per, dev),
-            p_held, p_held if n_pages_out is None else _want("n_pages_out", n_pages_out, _I32, per, dev),
-            _want("block_table", block_table, _I32, table_shape, dev), _want("free_list", free_list, _I32, pages, dev),
-            p_count, p_count if free_count_out is None else _want("free_count_out", free_count_out, _I32, one, dev),
-            _want("kv_len", kv_len, _I32, per, dev), _want("q_len", q_len, _I32, per, dev),
-            _want("slot_map", slot_map, _I64, (B, T), dev))
-    status = _want("status_word", status_word, _I32, one, dev) or 0
-    shape = _pack_kv_shape(B, T, 1, 1, 64, GDN_BF16, GDN_BF16, page_size, pages[0], max_pages, 0, 0, 0, status)
+    *args, status = _pointers(_PLAN, dev, (B, max_pages, pages, T, 1), seq_len, seq_len if seq_len_out is None else seq_len_out,
+                              commit_len, block_len, add_len, n_pages, n_pages if n_pages_out is None else n_pages_out,
+                              block_table, free_list, free_count, free_count if free_count_out is None else free_count_out,
+                              kv_len, q_len, slot_map, status_word)
+    shape = _pack_kv_shape(B, T, 1, 1, 64, GDN_BF16, GDN_BF16, page_size, pages, max_pages, 0, 0, 0, status or 0)
     rc = _load().gdn_kv_plan(shape, *args, _raw_stream(stream, dev))
     if rc:
         _check(rc)
@@ -596,40 +623,39 @@ def rope_append(q, k, v, inv_freq, k_cache, v_cache, slot_map, positions=None, k
     each axis (None: one axis). Returns q_out (may be q)."""
     B, T, H_q, d = q_shape = q.shape
     H_kv = k.shape[2]
-    if k.shape != (B, T, H_kv, d) or v.shape != k.shape:
-        raise ValueError("q [B,T,H_q,d] and k, v [B,T,H_kv,d] disagree")
     dtype, dev = q.dtype, q.get_device()
-    if k.dtype is not dtype or v.dtype is not dtype:
-        raise TypeError("q, k, v must share a dtype")
-    page, pages, st = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
+    if q_out is None:
+        q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+    rows = _native().tokens(dtype, dev, B, T, d, q, H_q, k, H_kv, v, H_kv, q_out, H_q)
+    if rows is None:
+        if k.shape != (B, T, H_kv, d) or v.shape != k.shape:
+            raise ValueError("q [B,T,H_q,d] and k, v [B,T,H_kv,d] disagree")
+        if k.dtype is not dtype or v.dtype is not dtype:
+            raise TypeError("q, k, v must share a dtype")
+        if q_out.dtype is not dtype:
+            raise TypeError("q_out must have q's dtype")
+        if q_out.shape != q_shape:
+            raise ValueError("q_out must be %s, not %s" % (list(q_shape), list(q_out.shape)))
+        if k.get_device() != dev or v.get_device() != dev or q_out.get_device() != dev:
+            raise ValueError("k, v and q_out are not where q is")
+        rows = []
+        for name, t, H in (("q", q, H_q), ("k", k, H_kv), ("v", v, H_kv), ("q_out", q_out, H_q)):
+            rows += [_token_stride(name, t, B, T, H, d), t.data_ptr()]
+    s_q, p_q, s_k, p_k, s_v, p_v, s_out, p_out = rows
+    page, pages, page_stride, slot_stride, head_stride, p_kc, p_vc = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
     half = inv_freq.numel()
     n_axes = 1 if sections is None else len(sections)
     if not 1 <= n_axes <= 4:
         raise ValueError("one to four sections")
     sec = (half, 0, 0, 0) if sections is None else (*sections, 0, 0, 0)[:4]
-    if q_out is None:
-        q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
-    if q_out.dtype is not dtype:
-        raise TypeError("q_out must have q's dtype")
-    if q_out.shape != q_shape:
-        raise ValueError("q_out must be %s, not %s" % (list(q_shape), list(q_out.shape)))
-    if k.get_device() != dev or v.get_device() != dev or q_out.get_device() != dev:
-        raise ValueError("k, v and q_out are not where q is")
     if positions is not None:
         kv_len = q_len = None
-    per, heads = (B,), (d,)
-    args = (_want("inv_freq", inv_freq, _F32, (half,), dev), _want("positions", positions, _I32, (n_axes, B, T), dev),
-            _want("kv_len", kv_len, _I32, per, dev), _want("q_len", q_len, _I32, per, dev),
-            _want("slot_map", slot_map, _I64, (B, T), dev), _want("q_norm", q_norm, _F32, heads, dev),
-            _want("k_norm", k_norm, _F32, heads, dev))
+    *args, status = _pointers(_APPEND, dev, (B, T, half, n_axes, d, 1), inv_freq, positions, kv_len, q_len, slot_map, q_norm, k_norm,
+                              status_word)
     code = _dtype_code(dtype)
-    status = _want("status_word", status_word, _I32, (1,), dev) or 0
-    shape = _pack_kv_shape(B, T, H_q, H_kv, d, code, code, page, pages, 1, st[0], st[1], st[2], status)
-    rope = _pack_rope(2 * half, n_axes, *sec, 1 if axes_interleaved else 0, 1 if pairs_interleaved else 0, norm_eps,
-                      _token_stride("q", q, B, T, H_q, d), _token_stride("k", k, B, T, H_kv, d),
-                      _token_stride("v", v, B, T, H_kv, d), _token_stride("q_out", q_out, B, T, H_q, d))
-    rc = _load().gdn_rope_append(shape, rope, q.data_ptr(), k.data_ptr(), v.data_ptr(), *args, q_out.data_ptr(),
-                                 k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev))
+    shape = _pack_kv_shape(B, T, H_q, H_kv, d, code, code, page, pages, 1, page_stride, slot_stride, head_stride, status or 0)
+    rope = _pack_rope(2 * half, n_axes, *sec, 1 if axes_interleaved else 0, 1 if pairs_interleaved else 0, norm_eps, s_q, s_k, s_v, s_out)
+    rc = _load().gdn_rope_append(shape, rope, p_q, p_k, p_v, *args, p_out, p_kc, p_vc, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return q_out
@@ -651,28 +677,23 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=
     B, T, H_q, d = q_shape = q.shape
     dtype, dev = q.dtype, q.get_device()
     H_kv = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    page, pages, st = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
+    page, pages, page_stride, slot_stride, head_stride, p_kc, p_vc = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
     if o is None:
         o = torch.empty(q_shape, dtype=out_dtype or dtype, device=q.device)
     elif out_dtype is not None and o.dtype is not out_dtype:
         raise TypeError("o is %s but out_dtype is %s" % (o.dtype, out_dtype))
-    table_shape = block_table.shape
-    if len(table_shape) != 2 or table_shape[0] != B:
+    if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    per = (B,)
-    args = (_want("block_table", block_table, _I32, table_shape, dev), _want("kv_len", kv_len, _I32, per, dev),
-            _want("q_len", q_len, _I32, per, dev), _want("o", o, o.dtype, q_shape, dev),
-            _want("lse", lse, _F32, (B, T, H_q), dev))
-    p_q = _want("q", q, dtype, q_shape, dev)
-    status = _want("status_word", status_word, _I32, (1,), dev) or 0
-    shape = _pack_kv_shape(B, T, H_q, H_kv, d, _dtype_code(dtype), _dtype_code(o.dtype), page, pages, table_shape[1],
-                           st[0], st[1], st[2], status)
+    max_pages = block_table.shape[1]
+    code, out_code = _dtype_code(dtype), _dtype_code(o.dtype)
+    p_q, *args, status = _pointers(_ATTENTION[dtype, o.dtype], dev, (B, T, H_q, d, max_pages, 1), q, block_table, kv_len, q_len, o, lse,
+                                   status_word)
+    shape = _pack_kv_shape(B, T, H_q, H_kv, d, code, out_code, page, pages, max_pages, page_stride, slot_stride, head_stride, status or 0)
     lib = _load()
     if workspace is None:
         workspace = torch.empty(max(lib.gdn_paged_attention_workspace_bytes(shape), 16), dtype=torch.uint8, device=q.device)
     p_ws = _want("workspace", workspace, workspace.dtype, workspace.shape, dev)
-    rc = lib.gdn_paged_attention(shape, d ** -0.5 if scale is None else scale, window, p_q, k_cache.data_ptr(),
-                                 v_cache.data_ptr(), *args, p_ws, _nbytes(workspace), _raw_stream(stream, dev))
+    rc = lib.gdn_paged_attention(shape, d ** -0.5 if scale is None else scale, window, p_q, p_kc, p_vc, *args, p_ws, _nbytes(workspace), _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return o

@@ -173,3 +173,34 @@ def test_binding_refusals(gdn):
                     (dict(k_cache=bf(5, 16, 128)), "k_cache and v_cache must be"), (dict(), "expected a CUDA tensor")):
         with pytest.raises(ValueError, match=msg):
             attn(**kw)
+
+
+def test_native_checks_agree_with_the_slow_ones(gdn):
+    # the native look answers exactly where the tensor-by-tensor one does, with the same pointers
+    spec = (("a", torch.int32, (0, 1)), ("b", torch.float32, (1,)), ("c", torch.int64, (0,)))
+    a, b, c = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(3), torch.zeros(2, dtype=torch.int64)
+    native = gdn._native().pointers
+    slow = lambda *t: tuple(gdn._want(n, x, dt, tuple((2, 3)[i] for i in ax), -1) for (n, dt, ax), x in zip(spec, t))  # noqa: E731
+    assert native(spec, -1, (2, 3), a, b, None) == slow(a, b, None) == (a.data_ptr(), b.data_ptr(), None)
+    assert gdn._pointers(spec, -1, (2, 3), a, b, c) == slow(a, b, c)
+    for bad in ((a.long(), b, c), (a.t(), b, c), (a[:1], b, c), (a, b[:2], c), (a, b.double(), c), (a, b, c[:, None]),
+                (torch.zeros(3, 2, dtype=torch.int32).t(), b, c), (a, b, 5)):
+        assert native(spec, -1, (2, 3), *bad) is None
+    assert native(spec, 0, (2, 3), a, b, c) is None
+    for wrong in ((), (spec,), (spec, -1, (2, 3), a), (spec, -1, [2, 3], a, b, c)):
+        with pytest.raises(TypeError):
+            native(*wrong)
+    with pytest.raises(TypeError, match="a must be int32"):
+        gdn._pointers(spec, -1, (2, 3), b, b, c)
+
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    wide, k, v = bf(2, 5, 12, 64), bf(3, 2, 16, 64).transpose(1, 2), bf(3, 2, 16, 64).transpose(1, 2)
+    q = wide[:, :, 2:8]
+    assert gdn._native().tokens(torch.bfloat16, -1, 2, 5, 64, q, 6) == (gdn._token_stride("q", q, 2, 5, 6, 64), q.data_ptr())
+    for one in (bf(4, 1, 6, 64), bf(1, 1, 6, 64), wide[:1, :1, :6], wide[:, :1, :6]):
+        assert gdn._native().tokens(torch.bfloat16, -1, one.shape[0], 1, 64, one, 6)[0] == gdn._token_stride("q", one, one.shape[0], 1, 6, 64)
+    for t in (wide[:, :, ::2], wide[:, ::2, :6], wide[:, :, :6].float(), wide[..., :32], bf(5, 2, 6, 64).transpose(0, 1)):
+        assert gdn._native().tokens(torch.bfloat16, -1, 2, 5, 64, t, 6) is None
+    assert gdn._native().caches(k, v, torch.bfloat16, -1, 2, 64) == (16, 3, 2048, 64, 1024, k.data_ptr(), v.data_ptr())
+    for pair in ((k, v.contiguous()), (k.float(), v), (k[:2], v), (k[..., :32], v[..., :32]), (k[0], v[0])):
+        assert gdn._native().caches(*pair, torch.bfloat16, -1, 2, 64) is None
