@@ -6,7 +6,7 @@
 // every sequence's pages on the free list, so the result does not depend on any order of
 // execution. One CTA does it, a thread for each sequence, because every step hangs on the sums; it is a chain
 // of six dependent reads, bound by their latency: 3 us on the device for one sequence, 7.4 us for 256 of a block of 8
-// (11.7 us under a profiler, cold), 13 us and 3 for the slots of 32 prompts of up to 8192. The slots of a block of a few tokens are formed there
+// (11.7 us under a profiler, cold), 8.5 us in all with the slots of 32 prompts of up to 8192. The slots of a block of a few tokens are formed there
 // too; those of prompts (one each for tens of thousands of tokens) by a second kernel over all SMs,
 // launched as a programmatic dependent.
 #include <cuda_runtime.h>
@@ -25,7 +25,8 @@ constexpr int kMaxThreads = 1024;
 constexpr int kMaxWarps = kMaxThreads / 32;
 // Up to this many slots one CTA is faster than a second launch.
 constexpr int64_t kInlineSlots = 8192;
-// A lane copies up to this many pages of its own sequence; more are copied by the whole warp.
+// A thread copies up to this many pages of its own sequence; more are copied by a warp, the sequences dealt to
+// the block's warps in turn (32 prompts of up to 128 pages each: 18.4 us a call by the one warp that their threads are, 10.3 so).
 constexpr int kLanePages = 2;
 
 // One sequence's request. want == held where nothing can be done for it.
@@ -110,10 +111,10 @@ __device__ __forceinline__ void warp_copy(int n, int lane, From from, To to) {
 __global__ void __launch_bounds__(kMaxThreads) gdn_kv_plan_kernel(const __grid_constant__ KvPlanArgs a, bool slots_here) {
     __shared__ int64_t part[kMaxWarps];
     __shared__ unsigned long long s_granted;
-    __shared__ int s_len[kMaxThreads], s_q[kMaxThreads], s_held[kMaxThreads], s_k0[kMaxThreads];
+    __shared__ int s_len[kMaxThreads], s_q[kMaxThreads], s_held[kMaxThreads], s_k0[kMaxThreads], s_n[kMaxThreads];
     // the slot kernel may take its place on the SMs now; it waits for this one to end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int tiles = (a.B + nt - 1) / nt;
     int status = 0;
     int count = *a.count_in;
@@ -136,17 +137,20 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_kv_plan_kernel(const __grid_c
         const int back = max(s.held - s.want, 0);
         int64_t total;
         const int64_t at = carry + block_scan(back, part, &total) - back;
-        if (back <= kLanePages)
-            for (int i = 0; i < back; ++i)
-                if (at + i < a.num_pages) a.free_list[at + i] = a.table[(size_t)b * a.max_pages + s.want + i];
-        for (unsigned m = __ballot_sync(kFull, back > kLanePages); m; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int n = __shfl_sync(kFull, back, src), w0 = __shfl_sync(kFull, s.want, src);
-            const int64_t to = __shfl_sync(kFull, at, src);
-            const int32_t* row = a.table + (size_t)(b - lane + src) * a.max_pages + w0;
-            const int take = (int)min((int64_t)n, max((int64_t)0, a.num_pages - to));
-            warp_copy(take, lane, [&](int i) { return row[i]; }, [&](int i, int v) { a.free_list[to + i] = v; });
-        }
+        const int to = (int)min(at, (int64_t)a.num_pages), n = min(back, a.num_pages - to);
+        if (n <= kLanePages)
+            for (int i = 0; i < n; ++i) a.free_list[to + i] = a.table[(size_t)b * a.max_pages + s.want + i];
+        // (in these loops the arrays are the next tile's again behind its scan's barriers)
+        s_n[tid] = n;
+        s_k0[tid] = to;
+        s_held[tid] = s.want;
+        if (__syncthreads_or(n > kLanePages))
+            for (int j = warp; j < min(nt, a.B - tile * nt); j += nt / 32) {
+                if (s_n[j] <= kLanePages) continue;
+                const int32_t* from = a.table + (size_t)(tile * nt + j) * a.max_pages + s_held[j];
+                int32_t* onto = a.free_list + s_k0[j];
+                warp_copy(s_n[j], lane, [&](int i) { return from[i]; }, [&](int i, int v) { onto[i] = v; });
+            }
         carry += total;
     }
     const int64_t have = carry < a.num_pages ? carry : a.num_pages;
@@ -177,14 +181,15 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_kv_plan_kernel(const __grid_c
         const int take = granted ? need : 0;
         if (take <= kLanePages)
             for (int i = 0; i < take; ++i) a.table[(size_t)b * a.max_pages + s.held + i] = a.free_list[have - 1 - k0 - i];
-        for (unsigned m = __ballot_sync(kFull, take > kLanePages); m; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int n = __shfl_sync(kFull, take, src), h0 = __shfl_sync(kFull, s.held, src), k = __shfl_sync(kFull, k0, src);
-            int32_t* row = a.table + (size_t)(b - lane + src) * a.max_pages + h0;
-            const int32_t* top = a.free_list + (have - 1 - k);
-            warp_copy(n, lane, [&](int i) { return top[-i]; }, [&](int i, int v) { row[i] = v; });
-        }
-        __syncthreads();      // every thread has read this tile's counts: they may be written in place
+        s_n[tid] = take;
+        // every thread has read this tile's counts: they may be written in place
+        if (__syncthreads_or(take > kLanePages))
+            for (int j = warp; j < min(nt, a.B - b0); j += nt / 32) {
+                if (s_n[j] <= kLanePages) continue;
+                const int32_t* top = a.free_list + (have - 1 - s_k0[j]);
+                int32_t* row = a.table + (size_t)(b0 + j) * a.max_pages + s_held[j];
+                warp_copy(s_n[j], lane, [&](int i) { return top[-i]; }, [&](int i, int v) { row[i] = v; });
+            }
         if (b < a.B) {
             a.seq_out[b] = s.seq_out;
             a.held_out[b] = now;
@@ -245,7 +250,8 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
     const int64_t slots = (int64_t)a.B * a.T;
     const bool here = slots <= kInlineSlots;
     const int64_t busy = std::max<int64_t>(a.B, here ? slots : 0);
-    const int threads = (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, (busy + 31) / 32 * 32));
+    // prompts: every warp has pages to copy
+    const int threads = !here ? kMaxThreads : (int)std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, (busy + 31) / 32 * 32));
     gdn_kv_plan_kernel<<<1, threads, 0, stream>>>(a, here);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || here) return e;

@@ -4,9 +4,11 @@
 // Every element of q, k and v is read once and written once; the angles of a token (rot / 2 of
 // them) are the same for all its heads, so a CTA forms them once in shared memory: the product
 // position x frequency in fp64, reduced to a fraction of a turn there, cosine and sine in fp32.
-// Measured for 24,576 tokens of 48 heads, d 128, bf16, head norms, three axes (604 MB): 142 us, 65% of
-// the measured copy rate; the same kernel without its arithmetic takes 109 us, without the norm 128 us, without
-// the cosines no less; with 8 tokens per CTA 151 us, with 4 167 us, with 32 169 us. So it is bound by issue and HBM together. A block of a few tokens (8 x 32
+// Measured for 24,576 tokens of 48 heads, d 128, bf16, head norms, three axes (604 MB): 128 us, 72% of
+// the measured copy rate. The next token's rows are asked into L2 a token ahead (one bulk prefetch): 142 us
+// without, 130 and 135 with two and four ahead, 131 with the first tokens' asked for too. That earlier form took 109 us
+// without its arithmetic, 128 without the norm, no less without the cosines, so it was bound by issue and
+// the latency of HBM together; 151 with 8 tokens per CTA, 167 with 4, 169 with 32. A block of a few tokens (8 x 32
 // heads, d 256) takes 3.5 us, launch and three dependent reads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -22,8 +24,8 @@ using namespace dev;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Tokens from which on a CTA takes four, and sixteen. Measured with one, four, sixteen tokens per CTA (48 heads,
-// d 128, norms): 128 tokens 4.0, 8.1, 22 us; 256 6.3, 8.2, 23; 512 10.9, 8.4, 23; 4096 81, 30, 40; 8192
-// 163, 57, 52; 16,384 337, 104, 99 (20 heads, d 256, 8192 tokens: 160, 44, 39).
+// d 128, norms): 128 tokens 4.0, 8.8, 26 us; 256 6.4, 8.9, 26; 512 11.1, 9.2, 27; 4096 83, 30, 37; 6144 124, 42, 42;
+// 8192 165, 53, 50; 16,384 336, 98, 85 (20 heads, d 256: 4096 86, 26, 30; 8192 171, 45, 41).
 constexpr int kFour = 320, kSixteen = 6144;
 
 // Four elements as stored, and as fp32.
@@ -60,6 +62,11 @@ __device__ __forceinline__ void pack(const float (&x)[4], Raw4<__nv_bfloat16>& r
     r.u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 __device__ __forceinline__ void pack(const float (&x)[4], Raw4<float>& r) { r.u = make_float4(x[0], x[1], x[2], x[3]); }
+
+// Asks for `bytes` (16-byte units, as the address) to be brought into L2.
+__device__ __forceinline__ void ask_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 // The pair (a, b) turned by an angle.
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
@@ -152,6 +159,10 @@ __global__ void __launch_bounds__(kThreads, 4) gdn_rope_append_kernel(const __gr
             const int64_t cell = s_cell[tt];
             if (cell < 0) continue;                          // no slot: nothing of this token is written
             const E* from = src + tt * stride;
+            if (TT > 1 && group == 0 && lane == 0) {         // a token ahead of the loads below
+                const int ahead = tt + abreast;
+                if (ahead < TT && s_cell[ahead] >= 0) ask_l2(src + ahead * stride, heads * D * (int)sizeof(E));
+            }
             E* to = dst + (what == 0 ? (int64_t)(tok0 + tt) * a.qo_stride : cell);
             Raw4<E> r1[ITER], r2[ITER];
 #pragma unroll
