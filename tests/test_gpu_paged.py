@@ -432,6 +432,19 @@ def test_attention_unseen_values_by_place(gdn, tables, d, page):
     assert torch.equal(o, expect)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_long_fp32_sums_do_not_drift(gdn, d):
+    # With values of one, an output is its weights' sum over the same sum: 1 but for roundings. Those of 64
+    # additions that round have a deviation of sqrt(64) 2^-25 = 2.4e-7 at most, and their mean over 1024 rows one
+    # of 7.5e-9; sums that are cut instead of rounded all lose, 64 2^-25 = 1.9e-6 on average. 2^-22 lies between.
+    x = _attn_case(1, 16, 4, d, F32, 16, [4096] * 64, seed=d)
+    x["vc"].fill_(1.0)
+    o = torch.empty_like(x["q"])
+    gdn.paged_attention(x["q"], x["kc"], x["vc"], _i32(x["table"]), _i32(x["kv"]), o=o)
+    o = o.double()
+    assert float((o - 1).abs().max()) <= 2e-5 and abs(float((o - 1).mean())) <= 2.0 ** -22
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_attention_many_items_for_each_cta(gdn, tables, d):
     rng = np.random.default_rng(d)
