@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the mixer runs in the library's CUDA kernels.
 Tensors are PyTorch CUDA tensors used as device memory; the stream is the current torch
-stream unless one is given. There is no fallback: if libgdn.so is missing or a call fails,
-an exception is raised.
+stream unless one is given; then the caller sees to it that the inputs are ready there, and
+waits for it before reading the results. What a call allocates belongs to the stream it is
+launched on. There is no fallback: if libgdn.so is missing or a call fails, an exception is
+raised.
 
 Passages the entry points follow: the Gated DeltaNet mixer and its recurrent-state
 commit / rollback ("Lithos-metal: Qwen3.8-27B on 40-core M5 Max", table "GDN mixer" and
@@ -193,6 +195,27 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _torch_stream(stream, device):
+    """The stream a call is launched on, as PyTorch's allocator knows it (handles 0 and 1 are the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    return torch.cuda.default_stream(device) if handle in (None, 0, 1) else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """A tensor that a call makes itself. It belongs to the stream the call is launched on: its block's former
+    tenant is done there before the call's kernels begin, and its next one begins behind them, however early the
+    tensor is dropped. One that is ``returned`` is kept for the caller's current stream too, where it is read."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _shape_from(q, k, v, status_word, l2_eps, scale, out_dtype, launch_flags=0) -> _Shape:
     B, T, H_k, d_k = k.shape
     H_v, d_v = v.shape[2], v.shape[3]
@@ -252,7 +275,7 @@ def verify_step(q, k, v, a, b, A_log, dt_bias, state_in, state_out=None, accept_
     _dtypes(q, a, b, A_log, dt_bias, o, out_dtype,
             f32=(("state_in", state_in), ("state_out", state_out), ("stash", stash)), i32=(("accept_len", accept_len),))
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     if accept_len is not None and state_out is None:
         state_out = state_in
     _check(_load().gdn_verify_step(ctypes.byref(sh), *_ptrs(q, k, v, a, b, A_log, dt_bias, state_in, state_out,
@@ -284,7 +307,7 @@ def commit_and_verify(q, k, v, a, b, A_log, dt_bias, state, prev_stash, prev_acc
     _dtypes(q, a, b, A_log, dt_bias, o, out_dtype, f32=(("state", state), ("prev_stash", prev_stash), ("stash", stash)),
             i32=(("prev_accept_len", prev_accept_len), ("accept_len", accept_len)))
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     _check(_load().gdn_commit_and_verify(ctypes.byref(sh), int(prev_T),
                                          *_ptrs(q, k, v, a, b, A_log, dt_bias, state, prev_stash,
                                                 prev_accept_len, accept_len, o, stash),
@@ -304,7 +327,7 @@ def verify_step_gated(q, k, v, a, b, A_log, dt_bias, state_in, state_out, accept
     if norm_z.shape != v.shape or norm_z.dtype != v.dtype:
         raise ValueError("norm_z must have v's shape and dtype")
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     ptrs = _ptrs(q, k, v, a, b, A_log, dt_bias, state_in, state_out, accept_len, norm_z, norm_w, o, stash)
     _check(_load().gdn_verify_step_gated(ctypes.byref(sh), *ptrs[:12], float(norm_eps), *ptrs[12:], _stream(stream)))
     return o
@@ -317,7 +340,7 @@ def gated_rmsnorm(x, z, w, eps=1e-6, y=None, out_dtype=None, stream=None):
     if z.shape != x.shape or w.shape != (d,):
         raise ValueError("x, z [..., d] and w [d] disagree")
     if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        y = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
     _check(_load().gdn_gated_rmsnorm(x.numel() // d if d else 0, d, _ptr(x), _dtype_code(x.dtype), _ptr(z),
                                      _dtype_code(z.dtype), _ptr(w), float(eps), _ptr(y), _dtype_code(y.dtype),
                                      _stream(stream)))
@@ -343,12 +366,12 @@ def accept(target, tokens, draft=None, uniforms=None, temperature=1.0, workspace
     sampled = uniforms is not None
     sh = _accept_shape(B, T, V, target.dtype, sampled, temperature)
     if workspace is None:
-        workspace = torch.empty(max(accept_workspace_bytes(B, T, V, sampled, target.dtype), 16),
-                                dtype=torch.uint8, device=target.device)
+        workspace = _empty(max(accept_workspace_bytes(B, T, V, sampled, target.dtype), 16), torch.uint8, target.device, stream,
+                           returned=False)
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=target.device)
+        accept_len = _empty(B, torch.int32, target.device, stream)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=target.device)
+        next_token = _empty(B, torch.int32, target.device, stream)
     _check(_load().gdn_accept(ctypes.byref(sh),
                               *_ptrs(target, draft, tokens, uniforms, accept_len, next_token, workspace),
                               workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -383,9 +406,9 @@ def short_conv(q, k, v, conv_w, hist_in, hist_out=None, accept_len=None, outputs
     if hist_in.dtype != q.dtype or (hist_out is not None and hist_out.dtype != q.dtype):
         raise TypeError("the history has the dtype of q, k, v")
     if outputs:
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        v_out = torch.empty_like(v) if v_out is None else v_out
+        q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
+        v_out = _empty(v.shape, v.dtype, v.device, stream) if v_out is None else v_out
     else:
         q_out = k_out = v_out = None
     _check(_load().gdn_short_conv(ctypes.byref(sh), int(conv_w.shape[1]) if conv_w is not None else
@@ -402,7 +425,7 @@ def decode_step(q, k, v, a, b, A_log, dt_bias, state, o=None, l2_eps=1e-6, scale
     sh = _shape_from(q, k, v, status_word, l2_eps, scale, out_dtype, GDN_LAUNCH_PDL if pdl else 0)
     _dtypes(q, a, b, A_log, dt_bias, o, out_dtype, f32=(("state", state),))
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     _check(_load().gdn_decode_step(ctypes.byref(sh), *_ptrs(q, k, v, a, b, A_log, dt_bias, state, o),
                                    _stream(stream)))
     return o
@@ -420,12 +443,12 @@ def chunk_prefill(q, k, v, a, b, A_log, dt_bias, state_in=None, state_out=None, 
     B, T, H_k, d_k = k.shape
     H_v, d_v = v.shape[2], v.shape[3]
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     if state_out is None:
-        state_out = torch.empty((B, H_v, d_v, d_k), dtype=torch.float32, device=v.device)
+        state_out = _empty((B, H_v, d_v, d_k), torch.float32, v.device, stream)
     need = int(_load().gdn_chunk_prefill_workspace_bytes(ctypes.byref(sh), chunk))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=v.device)
+        workspace = _empty(need, torch.uint8, v.device, stream, returned=False)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(_load().gdn_chunk_prefill(ctypes.byref(sh), chunk,
                                      *_ptrs(q, k, v, a, b, A_log, dt_bias, state_in, state_out, o, workspace), wbytes,
@@ -464,9 +487,9 @@ def chunk_prefill_scan(v, workspace, H_k, state_in=None, state_out=None, o=None,
     if o is not None and o.dtype != out_dtype:
         raise TypeError("o is %s but out_dtype is %s" % (o.dtype, out_dtype))
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     if state_out is None:
-        state_out = torch.empty((B, H_v, d_v, d_k), dtype=torch.float32, device=v.device)
+        state_out = _empty((B, H_v, d_v, d_k), torch.float32, v.device, stream)
     _check(_load().gdn_chunk_prefill_scan(ctypes.byref(sh), chunk, *_ptrs(v, state_in, state_out, o, workspace),
                                           _nbytes(workspace), _stream(stream)))
     return o, state_out
@@ -488,9 +511,9 @@ def chunk_prefill_noalloc(q, k, v, a, b, A_log, dt_bias, state_in=None, state_ou
     B, T, H_k, d_k = k.shape
     H_v, d_v = v.shape[2], v.shape[3]
     if o is None:
-        o = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        o = _empty(v.shape, out_dtype, v.device, stream)
     if state_out is None:
-        state_out = torch.empty((B, H_v, d_v, d_k), dtype=torch.float32, device=v.device)
+        state_out = _empty((B, H_v, d_v, d_k), torch.float32, v.device, stream)
     _check(_load().gdn_chunk_prefill_noalloc(ctypes.byref(sh), chunk,
                                              *_ptrs(q, k, v, a, b, A_log, dt_bias, state_in, state_out, o),
                                              _stream(stream)))
@@ -596,11 +619,11 @@ def kv_plan(seq_len, n_pages, block_table, free_list, free_count, T, page_size, 
     pages = free_list.shape[0]
     dev = block_table.get_device()
     if kv_len is None:
-        kv_len = torch.empty(B, dtype=_I32, device=block_table.device)
+        kv_len = _empty(B, _I32, block_table.device, stream)
     if q_len is None:
-        q_len = torch.empty(B, dtype=_I32, device=block_table.device)
+        q_len = _empty(B, _I32, block_table.device, stream)
     if slot_map is None:
-        slot_map = torch.empty((B, T), dtype=_I64, device=block_table.device)
+        slot_map = _empty((B, T), _I64, block_table.device, stream)
     *args, status = _pointers(_PLAN, dev, (B, max_pages, pages, T, 1), seq_len, seq_len if seq_len_out is None else seq_len_out,
                               commit_len, block_len, add_len, n_pages, n_pages if n_pages_out is None else n_pages_out,
                               block_table, free_list, free_count, free_count if free_count_out is None else free_count_out,
@@ -625,7 +648,7 @@ def rope_append(q, k, v, inv_freq, k_cache, v_cache, slot_map, positions=None, k
     H_kv = k.shape[2]
     dtype, dev = q.dtype, q.get_device()
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+        q_out = _empty(q_shape, dtype, q.device, stream)
     rows = _native().tokens(dtype, dev, B, T, d, q, H_q, k, H_kv, v, H_kv, q_out, H_q)
     if rows is None:
         if k.shape != (B, T, H_kv, d) or v.shape != k.shape:
@@ -679,7 +702,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=
     H_kv = k_cache.shape[2] if k_cache.dim() == 4 else 0
     page, pages, page_stride, slot_stride, head_stride, p_kc, p_vc = _cache(k_cache, v_cache, H_kv, d, dtype, dev)
     if o is None:
-        o = torch.empty(q_shape, dtype=out_dtype or dtype, device=q.device)
+        o = _empty(q_shape, out_dtype or dtype, q.device, stream)
     elif out_dtype is not None and o.dtype is not out_dtype:
         raise TypeError("o is %s but out_dtype is %s" % (o.dtype, out_dtype))
     if block_table.dim() != 2 or block_table.shape[0] != B:
@@ -691,7 +714,7 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=
     shape = _pack_kv_shape(B, T, H_q, H_kv, d, code, out_code, page, pages, max_pages, page_stride, slot_stride, head_stride, status or 0)
     lib = _load()
     if workspace is None:
-        workspace = torch.empty(max(lib.gdn_paged_attention_workspace_bytes(shape), 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(lib.gdn_paged_attention_workspace_bytes(shape), 16), torch.uint8, q.device, stream, returned=False)
     p_ws = _want("workspace", workspace, workspace.dtype, workspace.shape, dev)
     rc = lib.gdn_paged_attention(shape, d ** -0.5 if scale is None else scale, window, p_q, p_kc, p_vc, *args, p_ws, _nbytes(workspace), _raw_stream(stream, dev))
     if rc:
