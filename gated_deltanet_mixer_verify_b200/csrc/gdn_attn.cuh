@@ -261,6 +261,21 @@ struct Sight {
     __device__ __forceinline__ bool partial(int pos, int n) const { return pos + n - 1 > p_min || pos < lo_max; }
 };
 
+// The values of column `col` at the positions from .. to - 1 of sequence b that are infinite or NaN, added up (0: none).
+// Out of line: only items that hold such values call it.
+template <typename E>
+__device__ __noinline__ float sum_non_numbers(const AttnArgs& a, int b, int h, int col, int from, int to) {
+    float sum = 0.f;
+    for (int pos = from; pos < to; ++pos) {
+        const int id = a.table[(int64_t)b * a.max_pages + pos / a.cache.page];
+        if ((unsigned)id >= (unsigned)a.cache.num_pages) continue;
+        const float y = dev::to_f(static_cast<const E*>(a.cache.v)[id * a.cache.page_stride + (int64_t)(pos % a.cache.page) * a.cache.slot_stride +
+                                                                  h * a.cache.head_stride + col]);
+        if (!isfinite(y)) sum += y;
+    }
+    return sum;
+}
+
 // The last word on one element of a row: weights w, their sum, and where it goes.
 __device__ __forceinline__ void store_o(const AttnArgs& a, int64_t at, float x) {
     if (a.out_bf16) dev::st_out<__nv_bfloat16>(a.o, at, x);

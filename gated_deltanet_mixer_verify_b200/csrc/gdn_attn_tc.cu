@@ -33,6 +33,8 @@
 // Steps, the first of these cases, us: rows as M, one thread per row, P in tensor memory 71; positions as M with the
 // steps of a tile one after the other 68; overlapped, and the join's grid small 56; programmatic dependents 51 to 54;
 // the look in rows at once, the next queries before the last look, items weighted 3 46.
+// What lies behind a sequence in its last page costs the look at up to 15 positions and the call 9% if all of it is NaN (the
+// second case: 115.0 us, 125.0; d 128 81.2, 89.0; d 64 77.8, 85.0).
 // Not faster: fetching with cp.async (5,600 to 9,800 cycles a tile; the proxy fence waits for copies in flight).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -189,7 +191,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     __shared__ alignas(16) float s_use[G::kGroups][32], s_k[G::kGroups][32];   // the same, 0 for none; factors
     __shared__ int64_t s_row[G::kGroups][32];      // where a row goes (-1: nowhere)
     __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_lost, s_not_numbers;
+    __shared__ volatile int s_lost;
+    __shared__ volatile int s_not_numbers;         // the last item with values that some row sees taken out of its tiles
     __shared__ uint32_t s_ask, s_looked;           // V tiles to be looked over, and looked over (counts)
     const AttnArgs& a = x.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -255,9 +258,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         // forgotten: while the first keys are on their way, it brings the instructions in (4,000 cycles of misses).
         uint32_t g = ~0u;
         bool fine = true;
+        int item = 0;                                            // counted from 1
         float l[32];
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
+            ++item;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
             for (int j = g == ~0u ? -1 : 0; j < n; ++j, ++g) {
@@ -391,7 +396,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             if (!(fine = product_done(g - 1))) break;
             tc::fence_after_sync();
             if (chunks > 0) {
-                const bool repair = s_not_numbers != 0;
+                const bool repair = s_not_numbers == item;
+                const int end = min(w.s.kv, first + n * kTile);
 #pragma unroll 1
                 for (int i = 0; i < G::kMb * chunks; ++i) {
                     const int mb = i / chunks, q = i - mb * chunks, col = mb * 128 + k;
@@ -399,21 +405,14 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     tc::tmem_ld16(lanes + G::kO + mb * (64 * NB) + 32 * wg + q * 16, o);
                     if (col >= D) continue;                      // d = 64: the upper lanes hold it twice
                     if (repair) {
-                        // what was taken out of the tiles (see the look below): to the rows that see it
-                        const int end = min(w.s.kv, first + n * kTile);
-                        for (int pos = max(first, see.lo_min); pos < end; ++pos) {
-                            if (pos >= see.lo_max && pos <= see.p_min) continue;   // seen by all: nothing was taken out
-                            const int id = a.table[(int64_t)w.b * a.max_pages + pos / a.cache.page];
-                            if ((unsigned)id >= (unsigned)a.cache.num_pages) continue;
-                            const float y = __bfloat162float(
-                                static_cast<const __nv_bfloat16*>(a.cache.v)[id * a.cache.page_stride + (int64_t)(pos % a.cache.page) * a.cache.slot_stride +
-                                                                             w.h * a.cache.head_stride + col]);
-                            if (isfinite(y)) continue;
-                            const int64_t from = (int64_t)max(0, pos - see.p0) * share - my_row0 - q * 16;
-                            const int64_t to = a.window > 0 ? ((int64_t)pos - see.p0 + a.window) * share - my_row0 - q * 16 : 16;
+                        // What was taken out of the tiles (see the look below), to the rows that see it: at the
+                        // positions before lo_max, and at those behind p_min, a block's length each at most.
 #pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                if (r >= from && r < to) o[r] += y;
+                        for (int r = 0; r < 16; ++r) {
+                            const int p = see.p0 + (my_row0 + q * 16 + r) / share;
+                            const int lo = max(first, a.window > 0 ? p - a.window + 1 : 0), hi = min(end, p + 1);
+                            o[r] += sum_non_numbers<__nv_bfloat16>(a, w.b, w.h, col, lo, min(hi, see.lo_max));
+                            o[r] += sum_non_numbers<__nv_bfloat16>(a, w.b, w.h, col, max(lo, max(see.lo_max, see.p_min + 1)), hi);
                         }
                     }
                     int64_t to[16];
@@ -577,6 +576,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     if (!(fine = __all_sync(kFull, await_count(&s_looked, looked, &s_lost)))) break;
                 }
                 const uint64_t p_at = p_base + (g + j) % G::kPb * (2 * G::kP) / 16;
+                // steps of 16 positions; those behind the sequence are left out, and what is there with them
+                const int steps = __shfl_sync(kFull, min(kTile, max(w.s.kv - first - j * kTile, 1) + 15) / 16, 0);
 #pragma unroll
                 for (int mb = 0; mb < G::kMb; ++mb) {
                     if (!(fine = await_warp(&bars.kv_full[slot], phase, &s_lost))) break;
@@ -584,10 +585,18 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     if (elect_one()) {
                         // d = 64: the second 64 rows of M are the first again (a stride of 0)
                         const uint64_t v_at = tc::desc_mnmajor_sw128(ring_at + slot * G::kSlot, G::kPer == 2 ? kBlock : 0);
-#pragma unroll
-                        for (int i = 0; i < 2 * kTile / 16; ++i)   // the leading term of P, then the other
+                        auto step = [&](int i) {                   // the leading term of P, then the other
                             tc::mma_bf16_ss(tm + G::kO + mb * (64 * NB), v_at + (i & 7) * 2048 / 16, p_at + ((i >> 3) * G::kP + (i & 7) * 2048) / 16,
                                             id_o, j > 0 || i > 0);
+                        };
+                        if (steps == kTile / 16) {
+#pragma unroll
+                            for (int i = 0; i < 2 * kTile / 16; ++i) step(i);
+                        } else {
+#pragma unroll 1
+                            for (int i = 0; i < 2 * kTile / 16; ++i)
+                                if ((i & 7) < steps) step(i);
+                        }
                         tc::mma_commit(&bars.kv_empty[slot]);
                         if (mb == G::kMb - 1) {
                             tc::mma_commit(&bars.pv_done[(g + j) & 1]);
@@ -637,7 +646,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             return true;
         };
         bool more = next_item();
-        while (more) {
+        for (int item = 1; more; ++item) {
             const int kv = w.s.kv, n = w.i1 - w.i0, first = w.s.first + w.i0 * kTile;
             const Sight see(a, w.s, row0, row0 + rows, share);
             // Values that are not numbers, at positions that some row does not see, would reach that row
@@ -650,8 +659,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 if (!fine || !see.partial(pos, kTile)) continue;
                 if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, &s_lost)))) break;
                 const uint32_t v_slot = slot0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kMb;   // V's first
-                // rows 0 .. low - 1 and high .. stop - 1 of the tile; behind them TMA has left zeros
-                const int stop = min(kTile, (max(kv - pos, 0) + run - 1) / run * run);
+                // rows 0 .. low - 1 and high .. stop - 1 of the tile; behind them TMA has left zeros, or the product stops
+                const int behind = max(kv - pos, 0), stop = min(kTile, min((behind + run - 1) / run * run, (behind + 15) / 16 * 16));
                 const int low = min(max(see.lo_max - pos, 0), stop), high = min(max(see.p_min + 1 - pos, low), stop);
                 const int ch = lane % G::kCpr, r_lane = lane / G::kCpr;
                 unsigned char* const v_at = ring + (v_slot + ch / (8 * G::kPer)) % G::kSlots * G::kSlot;
@@ -674,7 +683,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         const int r = r0 + r_lane + e * kQRows;
                         const uint4 z = make_uint4(numbers(y[e].x), numbers(y[e].y), numbers(y[e].z), numbers(y[e].w));
                         if ((r >= low && r < high) || (z.x == y[e].x && z.y == y[e].y && z.z == y[e].z && z.w == y[e].w)) continue;
-                        s_not_numbers = 1;
+                        // (behind the sequence, or before what any row sees: nobody's)
+                        if (pos + r < kv && pos + r >= see.lo_min) s_not_numbers = item;
                         *reinterpret_cast<uint4*>(v_at + tile_chunk(kTile, r, ch % (8 * G::kPer))) = z;
                     }
                 }

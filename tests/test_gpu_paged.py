@@ -433,6 +433,32 @@ def test_attention_unseen_values_by_place(gdn, tables, d, page):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_stale_slots_cost_nothing(gdn, d):
+    # what a page holds behind a sequence's length may be anything, and is looked at only there: a call over slots
+    # full of NaN takes as long as one over zeros (each the best of five, so a factor of 1.5 is noise enough; walking
+    # the items in search of such values took 4 to 6 times as long)
+    def us(x):
+        kv, table, o = _i32(x["kv"]), _i32(x["table"]), torch.empty_like(x["q"])
+        ws = torch.empty(gdn.paged_attention_workspace_bytes(*x["q"].shape[:3], 4, d), dtype=torch.uint8, device="cuda")
+        call = lambda: gdn.paged_attention(x["q"], x["kc"], x["vc"], table, kv, o=o, workspace=ws)  # noqa: E731
+        call()
+        best = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 100)
+        return best, o
+
+    lens = [100 + 8000 * i // 31 for i in range(32)]
+    (clean, o0), (nan, o1) = (us(_attn_case(8, 24, 4, d, BF, 64, lens, seed=1, stale=s)) for s in (0.0, float("nan")))
+    assert torch.equal(o0, o1) and nan <= 1.5 * clean, (clean, nan)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_attention_long_fp32_sums_do_not_drift(gdn, d):
     # With values of one, an output is its weights' sum over the same sum: 1 but for roundings. Those of 64
     # additions that round have a deviation of sqrt(64) 2^-25 = 2.4e-7 at most, and their mean over 1024 rows one
