@@ -261,6 +261,15 @@ __device__ __forceinline__ void products(const float*, const float (&p)[MT][2][4
     }
 }
 
+// q k of row `row` and position `pos` of a stage, for a score whose tf32 terms gave NaN: one of an infinity is the
+// infinity less itself. In plain fp32 it is what the formula gives, an infinity or a number among it.
+template <int D>
+__device__ __noinline__ float plain_score(const unsigned char* q, const unsigned char* k, int row, int pos) {
+    float s = 0.f;
+    for (int i = 0; i < D; ++i) s = fmaf(element<float, D>(q, row, i), element<float, D>(k, pos, i), s);
+    return s;
+}
+
 // For a stage whose values are not all numbers while some row does not see all of its positions: 0
 // times infinity would reach that row in the product. So what is not a number goes straight to
 // the sums of the rows that see it, and leaves a zero in the stage; the product that follows is the
@@ -274,8 +283,9 @@ __device__ __forceinline__ void take_out_non_numbers(unsigned char* v, const uin
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float x = element<E, D>(v, key, 8 * i + 2 * (lane & 3) + e);
-                if (isfinite(x)) continue;
+                float x = element<E, D>(v, key, 8 * i + 2 * (lane & 3) + e);
+                if (is_number<E>(x)) continue;
+                x = as_infinite(x);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     if (seen[m][0] >> key & 1) o[m][i][e] += x;
@@ -284,7 +294,7 @@ __device__ __forceinline__ void take_out_non_numbers(unsigned char* v, const uin
             }
     __syncwarp();
     for (int i = lane; i < 16 * D; i += 32)
-        if (!isfinite(element<E, D>(v, i / D, i % D))) set_zero<E, D>(v, i / D, i % D);
+        if (!is_number<E>(element<E, D>(v, i / D, i % D))) set_zero<E, D>(v, i / D, i % D);
     __syncwarp();
 }
 
@@ -435,6 +445,19 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
                                     if (!(bits >> (8 * j + 2 * (lane & 3) + e) & 1)) p[i][j][2 * r + e] = -INFINITY;
                         }
                     }
+                    if constexpr (sizeof(E) == 4) {
+                        // (what is not seen is -infinity by now)
+                        if (isnan(((p[i][0][0] + p[i][0][1]) + (p[i][0][2] + p[i][0][3])) + ((p[i][1][0] + p[i][1][1]) + (p[i][1][2] + p[i][1][3])))) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (isnan(p[i][j][e]))
+                                        p[i][j][e] = x.c * plain_score<D>(q_tile, ring + stage * G::kStage, 16 * i + (lane >> 2) + 4 * (e & 2),
+                                                                          8 * j + 2 * (lane & 3) + (e & 1));
+                        }
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float top = fmaxf(fmaxf(p[i][0][2 * r], p[i][0][2 * r + 1]), fmaxf(p[i][1][2 * r], p[i][1][2 * r + 1]));
@@ -463,7 +486,7 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
                 if (!all) {
                     unsigned char* v = ring + stage * G::kStage + G::kStage / 2;
                     bool numbers = true;
-                    for (int i = lane; i < 16 * D; i += 32) numbers &= isfinite(element<E, D>(v, i / D, i % D));
+                    for (int i = lane; i < 16 * D; i += 32) numbers &= is_number<E>(element<E, D>(v, i / D, i % D));
                     if (!__all_sync(kFull, numbers)) take_out_non_numbers<E, D, MT>(v, seen, lane, o);
                 }
                 products<D, MT>(static_cast<const E*>(nullptr), p, v_at, lane, o);
@@ -509,10 +532,21 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
                 sum = fmaf(k, s_l[j][r], sum);
                 fma4(y, k, *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + j * G::kRing) + r * D + col));
             }
+            if (isnan((y.x + y.y) + (y.z + y.w)) && !isnan(sum)) {
+                const int pr = p0 + t, from = max(first, a.window > 0 ? pr - a.window + 1 : 0), to = min(min(s.kv, pr + 1), s.first + i1 * G::kUnit);
+                float* const e[4] = {&y.x, &y.y, &y.z, &y.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!isnan(*e[j])) continue;
+                    const float z = sum_non_numbers<E>(a, b, h, col + j, from, to);
+                    if (z != 0.f) *e[j] = z;
+                }
+            }
             if (w.whole) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = 1.f / sum;
+                if (sum == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int64_t out = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
-                store_o4(a, out * D + col, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                store_o4(a, out * D + col, sum == 0.f ? y : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
                 if (col == 0 && a.lse) a.lse[out] = (use + log2f(sum)) * kLn2;
             } else {
                 *reinterpret_cast<float4*>(x.parts.o + (part + r) * D + col) = y;

@@ -261,21 +261,38 @@ struct Sight {
     __device__ __forceinline__ bool partial(int pos, int n) const { return pos + n - 1 > p_min || pos < lo_max; }
 };
 
-// The values of column `col` at the positions from .. to - 1 of sequence b that are infinite or NaN, added up (0: none).
-// Out of line: only items that hold such values call it.
+// Values that are infinite or NaN. fp32: from 2^127 (2 - 2^-11) on, where the leading tf32 term is infinite, a value is
+// taken for infinite itself.
+template <typename E>
+__device__ __forceinline__ bool is_number(float x) { return fabsf(x) < (sizeof(E) == 4 ? 0x1.ffep127f : INFINITY); }
+__device__ __forceinline__ float as_infinite(float x) { return isnan(x) ? x : copysignf(INFINITY, x); }
+
+// The products cannot be trusted with such a value: the two terms of its weight may be zero, or of unlike signs, and zero
+// times infinity or a difference of infinities is NaN. So a sum that came out NaN while its row's weights are numbers is looked up again:
+// what the values of column `col` at the positions from .. to - 1 of sequence b that are no numbers add up to (0: there
+// are none), every weight taken as positive. Out of line: only items that hold such values call it, eight reads at once.
 template <typename E>
 __device__ __noinline__ float sum_non_numbers(const AttnArgs& a, int b, int h, int col, int from, int to) {
+    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    const E* v = static_cast<const E*>(a.cache.v) + h * a.cache.head_stride + col;
+    int page = max(from, 0) / a.cache.page, slot = max(from, 0) - page * a.cache.page;
     float sum = 0.f;
-    for (int pos = from; pos < to; ++pos) {
-        const int id = a.table[(int64_t)b * a.max_pages + pos / a.cache.page];
-        if ((unsigned)id >= (unsigned)a.cache.num_pages) continue;
-        const float y = dev::to_f(static_cast<const E*>(a.cache.v)[id * a.cache.page_stride + (int64_t)(pos % a.cache.page) * a.cache.slot_stride +
-                                                                  h * a.cache.head_stride + col]);
-        if (!isfinite(y)) sum += y;
+    for (int pos = max(from, 0); pos < to && !isnan(sum); pos += 8) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            y[k] = 0.f;
+            if (pos + k >= to) continue;
+            const int id = table[page];
+            if ((unsigned)id < (unsigned)a.cache.num_pages) y[k] = dev::to_f(v[id * a.cache.page_stride + (int64_t)slot * a.cache.slot_stride]);
+            if (++slot == a.cache.page) slot = 0, ++page;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (!is_number<E>(y[k])) sum += as_infinite(y[k]);
     }
     return sum;
 }
-
 // The last word on one element of a row: weights w, their sum, and where it goes.
 __device__ __forceinline__ void store_o(const AttnArgs& a, int64_t at, float x) {
     if (a.out_bf16) dev::st_out<__nv_bfloat16>(a.o, at, x);

@@ -26,6 +26,10 @@ struct Sum {
     float m, l, o[N];
 };
 
+// 2^x, but never 0: a part's sums may be infinite (a value was), and stay so however small its weight. A part this far
+// below the others adds 2^-126 of itself at most.
+__device__ __forceinline__ float weight(float x) { return fmaxf(exp2_approx(x), 0x1p-126f); }
+
 // Parts p0, p0 + step, ... below end of one row.
 template <int D>
 __device__ __forceinline__ void add_parts(const Args& x, const Deal& deal, int C, int tile, int r, const Lead& it, int p0, int step,
@@ -54,13 +58,13 @@ __device__ __forceinline__ void add_parts(const Args& x, const Deal& deal, int C
 #pragma unroll
         for (int f = 0; f < F; ++f) top = fmaxf(top, pm[f]);
         const float use = top == -INFINITY ? 0.f : top;
-        const float k = exp2_approx(s.m - use);
+        const float k = weight(s.m - use);
         s.l *= k;
 #pragma unroll
         for (int i = 0; i < N; ++i) s.o[i] *= k;
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            const float w = exp2_approx(pm[f] - use);
+            const float w = weight(pm[f] - use);
             s.l = fmaf(w, pl[f], s.l);
 #pragma unroll
             for (int i = 0; i < N; ++i) s.o[i] = fmaf(w, po[f][i], s.o[i]);
@@ -115,9 +119,9 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
         add_parts<D>(x, deal, C, tile, r, it, it.c0 + (together ? warp : 0), together ? kWarps : 1, lane, s);
         const int64_t out = ((int64_t)it.b * a.T + t) * a.Hq + (int64_t)it.h * G + (row - t * G);
         if (!together) {
-            const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+            const float inv = 1.f / s.l;                         // (l = 0: o = 0)
 #pragma unroll
-            for (int e = 0; e < N; ++e) store_o(a, out * D + e * 32 + lane, s.o[e] * inv);
+            for (int e = 0; e < N; ++e) store_o(a, out * D + e * 32 + lane, s.l == 0.f ? 0.f : s.o[e] * inv);
             if (lane == 0 && a.lse) a.lse[out] = ((s.m == -INFINITY ? 0.f : s.m) + log2f(s.l)) * kLn2;
             continue;
         }
@@ -136,15 +140,15 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
         float sum = 0.f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            f[w] = exp2_approx(s_m[w] - use);
+            f[w] = weight(s_m[w] - use);
             sum = fmaf(f[w], s_l[w], sum);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = 1.f / sum;
         for (int e = threadIdx.x; e < D; e += kThreads) {
             float y = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) y = fmaf(f[w], s_o[w][e], y);
-            store_o(a, out * D + e, y * inv);
+            store_o(a, out * D + e, sum == 0.f ? 0.f : y * inv);
         }
         if (threadIdx.x == 0 && a.lse) a.lse[out] = (use + log2f(sum)) * kLn2;
     }

@@ -174,6 +174,39 @@ __device__ __forceinline__ float reduce32(float* v, int lane) {
     return v[0];
 }
 
+// The outputs (or parts of them) in column `col` of n rows from `row` on, as just stored, over positions first .. end - 1
+// with values among them that are no numbers: what was taken out of the tiles (`repair`, see the look below) goes to the rows that
+// see it, and sums that such values turned into NaN are looked up again. The first stands at the positions before
+// lo_max and behind p_min, a block's length each at most; what all rows see stands between. to: where the rows
+// were stored (-1: nowhere); k: what they were scaled with (0 or NaN where the sums of their weights are).
+__device__ __noinline__ void mend(const Args& x, int b, int h, int col, int first, int end, Sight see, int share, int row, int n, bool repair, bool whole,
+                                  const int64_t* to, const float* k) {
+    using E = __nv_bfloat16;
+    const AttnArgs& a = x.a;
+    const bool half = whole && a.out_bf16;
+    float* const out = whole ? static_cast<float*>(a.o) : x.parts.o;
+    auto at = [&](int r) { return to[r] * a.d + col; };
+    auto stored = [&](int r) { return half ? __bfloat162float(static_cast<const E*>(a.o)[at(r)]) : out[at(r)]; };
+    bool lost = false;                                           // a sum is not a number though its weights are
+    for (int r = 0; r < n; ++r)
+        if (to[r] >= 0 && k[r] >= 0.f) lost |= isnan(stored(r));
+    if (!lost && !repair) return;
+    const float all = lost ? sum_non_numbers<E>(a, b, h, col, max(first, see.lo_max), min(end, see.p_min + 1)) : 0.f;
+    for (int r = 0; r < n; ++r) {
+        if (to[r] < 0 || !(k[r] >= 0.f)) continue;
+        const int p = see.p0 + (row + r) / share;
+        const int from = max(first, a.window > 0 ? p - a.window + 1 : 0), stop = min(end, p + 1);
+        const float y = sum_non_numbers<E>(a, b, h, col, from, min(stop, see.lo_max)) +
+                        sum_non_numbers<E>(a, b, h, col, max(from, max(see.lo_max, see.p_min + 1)), stop);
+        float o = stored(r);
+        if (k[r] == 0.f) o = 0.f;
+        else if (!isnan(o)) o += y;
+        else if (y + all != 0.f) o = y + all;
+        if (half) static_cast<E*>(a.o)[at(r)] = __float2bfloat16_rn(o);
+        else out[at(r)] = o;
+    }
+}
+
 // grid (C, row tiles of 64 NB). run: slots per copy, the largest power of two up to a tile that
 // divides the page size.
 template <int D, int NB>
@@ -278,7 +311,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     tc::tmem_ld16x2(S, S + 16, *reinterpret_cast<float(*)[16]>(s), *reinterpret_cast<float(*)[16]>(s + 16));
                     if (x.c <= 0.f) {                            // c enters the exponents as |c|
 #pragma unroll
-                        for (int r = 0; r < 32; ++r) s[r] = x.c < 0.f ? -s[r] : 0.f;
+                        for (int r = 0; r < 32; ++r) s[r] = x.c < 0.f ? -s[r] : s[r] * 0.f;
                     }
                     const int pos = first + j * kTile + k;
                     const uint32_t mask = *const_cast<const volatile uint32_t*>(&s_mask[g % kMaskRing][warp & 3]);
@@ -389,7 +422,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         }
                     }
                     s_row[wg][k] = to;
-                    s_k[wg][k] = !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                    s_k[wg][k] = isnan(sum) ? sum : !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
                 }
                 named_barrier_sync(bar, 128);
             }
@@ -404,23 +437,14 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     float o[16];
                     tc::tmem_ld16(lanes + G::kO + mb * (64 * NB) + 32 * wg + q * 16, o);
                     if (col >= D) continue;                      // d = 64: the upper lanes hold it twice
-                    if (repair) {
-                        // What was taken out of the tiles (see the look below), to the rows that see it: at the
-                        // positions before lo_max, and at those behind p_min, a block's length each at most.
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int p = see.p0 + (my_row0 + q * 16 + r) / share;
-                            const int lo = max(first, a.window > 0 ? p - a.window + 1 : 0), hi = min(end, p + 1);
-                            o[r] += sum_non_numbers<__nv_bfloat16>(a, w.b, w.h, col, lo, min(hi, see.lo_max));
-                            o[r] += sum_non_numbers<__nv_bfloat16>(a, w.b, w.h, col, max(lo, max(see.lo_max, see.p_min + 1)), hi);
-                        }
-                    }
                     int64_t to[16];
                     float f[16];
+                    float odd[4] = {};                           // NaN if one of them is no number
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         to[r] = s_row[wg][q * 16 + r] < 0 ? -1 : s_row[wg][q * 16 + r] * D + col;
                         f[r] = o[r] * s_k[wg][q * 16 + r];
+                        odd[r & 3] = fmaf(f[r], 0.f, odd[r & 3]);
                     }
                     if (!w.whole || !a.out_bf16) {
                         float* out = w.whole ? static_cast<float*>(a.o) : x.parts.o;
@@ -433,6 +457,9 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         for (int r = 0; r < 16; ++r)
                             if (to[r] >= 0) out[to[r]] = __float2bfloat16_rn(f[r]);
                     }
+                    if (repair || isnan((odd[0] + odd[1]) + (odd[2] + odd[3])))
+                        mend(x, w.b, w.h, col, first, end, see, share, my_row0 + q * 16, min(16, my_rows - q * 16), repair, w.whole,
+                             &s_row[wg][q * 16], &s_k[wg][q * 16]);
                 }
                 named_barrier_sync(bar, 128);                    // s_row, s_k and s_part are the next item's
             }

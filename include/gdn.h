@@ -513,8 +513,10 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  * stands at position p = kv_len[b] - q_len[b] + t and sees positions max(0, p - window + 1) .. p
  * (window 0: from 0). For query head h, with key head h / (H_q / H_kv):
  *   s_j = scale q . k_j,   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = ln sum_j e^{s_j}
- * A row that sees nothing (p < 0) gives o = 0 and lse = -infinity. What a row does not see cannot
- * change it, infinities and NaN included.
+ * A row that sees nothing (p < 0), or only scores of -infinity, gives o = 0 and lse = -infinity. What a row does not
+ * see cannot change it, infinities and NaN included. An infinite value that a row sees makes its column of the row's
+ * output that infinity, however small its weight (NaN: a NaN among them, or both infinities); a score of -infinity weighs
+ * nothing; a score that is +infinity or NaN makes the whole row NaN.
  *   q        [B][T][H_q][d] dtype (contiguous), o the same in out_dtype, lse [B][T][H_q] fp32 or NULL.
  *   block_table [B][max_pages] int32, kv_len [B] int32, q_len [B] int32 or NULL (T rows each).
  *   Rows t >= q_len[b] are left as they were in o and lse. A sequence with kv_len[b] outside
@@ -524,7 +526,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  *              calls that may overlap on the GPU need one each (two captured graphs included).
  * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products
  * with v as two bf16 terms (2^-17 relative). fp32 products are formed from split tf32 terms
- * (about 2^-22; finite values above 2^127 (2 - 2^-12) count as infinite). The result does not depend on the order in which CTAs finish.
+ * (about 2^-22; finite values of v from 2^127 (2 - 2^-11) on count as infinite). The result does not depend on the order in which CTAs finish.
  * shape: B 0..65535, T 1..16, d 64, 128 or 256, H_q <= 65535.
  */
 gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,

@@ -459,6 +459,132 @@ def test_attention_stale_slots_cost_nothing(gdn, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,window", [(8, 0), (16, 5), (8, 700)])
+def test_attention_seen_infinities_item_by_item(gdn, tables, d, T, window):
+    # a visible infinity in some sequences only, among many that one CTA works through: the ones behind it are as they
+    # were, and it reaches exactly the rows that see it
+    rng = np.random.default_rng([d, T])
+    lens = rng.integers(T, 300, 200).tolist()
+    x = _attn_case(T, 24, 4, d, BF, 8, lens, seed=d)
+    clean, _ = _run_attn(gdn, x, window=window)
+    expect = clean.clone()
+    for b in range(0, 200, 3):
+        n, h, col = lens[b], int(rng.integers(4)), int(rng.integers(d))
+        t = int(rng.integers(T))
+        pos = n - T + t                              # row t's own position: the rows from t on see it
+        x["vc"][x["table"][b, pos // 8], pos % 8, h, col] = float("inf")
+        last = T if window == 0 else min(T, t + window)
+        expect[b, t:last, 6 * h:6 * h + 6, col] = float("inf")
+    o, _ = _run_attn(gdn, x, window=window, check=False)
+    assert torch.equal(o, expect)
+
+
+def _same_with_non_numbers(x, o, lse, window=0):
+    """_check_attn where the definition gives infinities and NaN: those have to be the same, the rest within its bounds."""
+    with np.errstate(all="ignore"):
+        r, rl, written = paged.paged_attention(_f64(x["q"]), _f64(x["kc"]), _f64(x["vc"]), x["table"], x["kv"], x["ql"], None, window)
+    o64, l64 = _f64(o), _f64(lse)
+    for got, ref in ((o64[written], r[written]), (l64[written], rl[written])):
+        for kind in (np.isnan, np.isposinf, np.isneginf):
+            assert np.array_equal(kind(got), kind(ref)), kind
+    ok = written[..., None, None] & np.isfinite(r)
+    top = np.abs(_f64(x["vc"]))
+    top = top[np.isfinite(top) & (top < 1e30)].max()
+    bound = (4e-5 if x["q"].dtype == BF else 3e-5) * top + (2.0 ** -8 * np.abs(r) if o.dtype == BF else 0)
+    assert (np.abs(o64[ok] - r[ok]) <= np.broadcast_to(bound, r.shape)[ok]).all()
+    ok = written[..., None] & np.isfinite(rl)
+    assert (np.abs(l64[ok] - rl[ok]) <= 2e-5 + 2.0 ** -22 * np.abs(rl[ok])).all()
+    assert np.isfinite(r[written]).any() and not np.isfinite(r[written]).all()
+
+
+def _put(x, b, pos, h, col, val, what="vc"):
+    page = x["kc"].shape[1]
+    x[what][x["table"][b, pos // page], pos % page, h, col] = val
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,Hq,Hk,d", [(1, 4, 2, 128), (8, 12, 2, 64), (8, 12, 2, 128), (8, 6, 1, 256), (16, 16, 2, 64)])
+def test_attention_seen_values_that_are_no_numbers(gdn, tables, T, Hq, Hk, d, dt):
+    # where every row sees them, wherever they stand: infinities stay infinities, in their column, whether their item
+    # is one CTA's or many's; a NaN, or both infinities, give NaN
+    inf, nan = float("inf"), float("nan")
+    for lens in ([300, 40, 700, 129], [5000, 333]):
+        x = _attn_case(T, Hq, Hk, d, dt, 16, lens, seed=d + T)
+        rng = np.random.default_rng(d + T)
+        cols = rng.permutation(d)
+        for b, n in enumerate(lens):
+            for i, vals in enumerate(([inf], [-inf], [nan], [inf, -inf], [inf, inf, inf], [-inf, -inf], [inf, nan])):
+                for v in vals:
+                    _put(x, b, int(rng.integers(0, n - T)) if i else 0, int(rng.integers(Hk)) if len(vals) == 1 else 0, cols[i], v)
+        for window in (0, 64):
+            o, lse = _run_attn(gdn, x, window=window, check=False)
+            _same_with_non_numbers(x, o, lse, window)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,Hq,Hk,d", [(1, 4, 2, 128), (8, 12, 2, 64), (8, 12, 2, 128), (3, 6, 1, 256), (16, 16, 2, 64)])
+def test_attention_keys_that_are_no_numbers(gdn, tables, T, Hq, Hk, d, dt):
+    # an infinite element of a key is a score of plus or minus infinity by the query's sign: the row is NaN, or as if
+    # the position were not there; so is an infinite element of a query, and a NaN is a NaN
+    lens = [300, 40, 2500, 129]
+    for which in range(3):
+        x = _attn_case(T, Hq, Hk, d, dt, 16, lens, seed=d + T)
+        if which == 0:
+            for b, n in enumerate(lens):
+                _put(x, b, n // 2, b % Hk, 7 * b, float("-inf") if b % 2 else float("inf"), "kc")
+        elif which == 1:
+            _put(x, 1, 20, 0, 3, float("nan"), "kc")
+            _put(x, 2, 2490, 0, 5, float("-inf"), "kc")
+        else:
+            x["q"][0, T - 1, Hq - 1, 9] = float("inf")
+            x["q"][3, 0, 0, 1] = float("nan")
+        o, lse = _run_attn(gdn, x, check=False)
+        _same_with_non_numbers(x, o, lse)
+
+
+@pytest.mark.parametrize("T,Hq,dt", [(1, 4, BF), (8, 16, BF), (2, 4, F32)])
+def test_attention_scores_of_minus_infinity(gdn, tables, T, Hq, dt):
+    # keys that shut out all positions but some, and then all
+    x = _attn_case(T, Hq, 2, 128, dt, 16, [500, 64, 90], seed=3)
+    x["q"].abs_()
+    clean = {k: v.clone() for k, v in x.items() if k in ("kc", "vc")}
+    shut = np.ones(500, bool)
+    shut[[3, 77, 140, 299, 471]] = False
+    for pos in np.nonzero(shut)[0]:
+        _put(x, 0, pos, slice(None), 11, float("-inf"), "kc")
+    o, lse = _run_attn(gdn, x, check=False)
+    k, v = (_f64(clean[n])[x["table"][0]].reshape(-1, 2, 128)[:500] for n in ("kc", "vc"))
+    for t in range(T):
+        see = [p for p in (3, 77, 140, 299, 471) if p <= 500 - T + t]
+        for h in range(Hq):
+            g = h * 2 // Hq
+            s = k[see][:, g] @ _f64(x["q"])[0, t, h] / 128 ** 0.5
+            w = np.exp(s - s.max())
+            ref = w @ v[see][:, g] / w.sum()
+            assert (np.abs(_f64(o)[0, t, h] - ref) <= 4e-5 * 6 + 2.0 ** -8 * np.abs(ref)).all()
+            assert abs(float(lse[0, t, h]) - s.max() - np.log(w.sum())) <= 2e-5 + 2.0 ** -22 * 12
+    x["kc"][..., 11] = float("-inf")
+    o, lse = _run_attn(gdn, x, check=False)
+    assert not o.any() and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("T,Hq", [(4, 2), (8, 16)])
+@pytest.mark.parametrize("bad", [float("-inf"), torch.finfo(F32).max, torch.finfo(F32).min])
+def test_attention_unseen_largest_numbers(gdn, T, Hq, bad):
+    # fp32 slots behind the sequences, and the last draft's key and value, full of a type's largest or lowest number
+    x = _attn_case(T, Hq, 2, 64, F32, 16, [70, T, 130], seed=4, stale=0.0)
+    clean = _run_attn(gdn, x)
+    y = _attn_case(T, Hq, 2, 64, F32, 16, [70, T, 130], seed=4, stale=bad)
+    o, lse = _run_attn(gdn, y)
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+    for b, n in enumerate(y["kv"]):
+        _put(y, b, n - 1, slice(None), slice(None), bad, "kc")
+        _put(y, b, n - 1, slice(None), 3, bad)
+    o, lse = _run_attn(gdn, y, check=False)
+    assert torch.equal(o[:, :-1], clean[0][:, :-1]) and torch.equal(lse[:, :-1], clean[1][:, :-1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_attention_long_fp32_sums_do_not_drift(gdn, d):
     # With values of one, an output is its weights' sum over the same sum: 1 but for roundings. Those of 64
     # additions that round have a deviation of sqrt(64) 2^-25 = 2.4e-7 at most, and their mean over 1024 rows one
