@@ -333,11 +333,11 @@ gdn_paged_attention_kernel(const __grid_constant__ Args x) {
         const Seq& s = w.s;
         const int b = w.b, h = w.h, i0 = w.i0, i1 = w.i1;
 
-        // the item's query rows
+        // the item's query rows; zeros for rows behind the sequence's last, whatever q holds there
         for (int i = tid; i < 16 * MT * CPR; i += NT) {
             const int r = i / CPR, ch = i - r * CPR, row = row0 + r;
             uint4 z = make_uint4(0, 0, 0, 0);
-            if (row < all_rows) {
+            if (row < share * s.rows) {
                 const int t = row / share;
                 const int64_t qr = ((int64_t)b * a.T + t) * a.Hq + (int64_t)h * share + (row - t * share);
                 z = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + qr * G::kRow + ch * 16);

@@ -92,8 +92,9 @@ __device__ __forceinline__ uint32_t tile_chunk(int rows, int r, int ch) {
     return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    // a source size of 0 fills the 16 bytes with zeros and reads nothing
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Two bf16 values, with zeros for those that are infinite or NaN.
@@ -656,12 +657,13 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 if (!w.next(x)) return false;
             } while (row0 / share >= w.s.rows);
             if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, &s_lost))) return false;
-            const int ch = lane % G::kCpr;
+            // rows behind the sequence's last are zeros, whatever q holds there: the votes on the maxima are taken among all
+            const int ch = lane % G::kCpr, real = share * w.s.rows - row0;
             int r = lane / G::kCpr, t = (row0 + r) / share, head = row0 + r - t * share;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + head) * D + ch * 8;
 #pragma unroll 4
             for (; r < rows; r += kQRows) {
-                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), q);
+                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), q, r < real);
                 q += kQRows * D;
                 for (head += kQRows; head >= share; head -= share) q += (int64_t)(a.Hq - share) * D;   // the next token's
             }

@@ -519,7 +519,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  * nothing; a score that is +infinity or NaN makes the whole row NaN.
  *   q        [B][T][H_q][d] dtype (contiguous), o the same in out_dtype, lse [B][T][H_q] fp32 or NULL.
  *   block_table [B][max_pages] int32, kv_len [B] int32, q_len [B] int32 or NULL (T rows each).
- *   Rows t >= q_len[b] are left as they were in o and lse. A sequence with kv_len[b] outside
+ *   Rows t >= q_len[b] are left as they were in o and lse, and what q holds there changes nothing. A sequence with kv_len[b] outside
  *   0..max_pages * page_size or q_len[b] outside 0..T writes nothing (GDN_STATUS_BAD_LENGTH).
  *   Positions on a page id outside the pool are not seen (GDN_STATUS_BAD_PAGE).
  *   workspace  gdn_paged_attention_workspace_bytes, 16-byte aligned, contents irrelevant on entry;

@@ -432,6 +432,22 @@ def test_attention_unseen_values_by_place(gdn, tables, d, page):
     assert torch.equal(o, expect)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,Hq,d", [(8, 12, 64), (8, 12, 128), (16, 12, 256)])
+def test_attention_rows_behind_the_block_change_nothing(gdn, tables, T, Hq, d, dt):
+    # q's rows from q_len on are nobody's: the same bits whatever stands there
+    rng = np.random.default_rng(d)
+    lens = rng.integers(T, 900, 40).tolist()
+    x = _attn_case(T, Hq, 2, d, dt, 16, lens, q_len=rng.integers(0, T + 1, 40), seed=d)
+    behind = torch.arange(T, device="cuda")[None] >= _i32(x["ql"])[:, None]
+    want = None
+    for junk in (0.0, 1e4, float("nan"), float("-inf"), torch.finfo(dt).max):
+        x["q"][behind] = junk
+        got = _run_attn(gdn, x, check=want is None)
+        want = want or got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), junk
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_attention_stale_slots_cost_nothing(gdn, d):
     # what a page holds behind a sequence's length may be anything, and is looked at only there: a call over slots
