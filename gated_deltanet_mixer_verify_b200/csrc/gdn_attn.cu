@@ -26,7 +26,8 @@
 // they form short sums only, and ordinary additions, which round, put those together.
 // Measured, 64 sequences of 4096 positions, 16 heads over 4, values of one, mean error of the outputs (formed in the units:
 // all in them): d 64 -5.9e-8 (-1.4e-6), 136 us (133); d 128 -6.5e-8 (-1.8e-6), 371 us (342); d 256 -5.8e-8
-// (-2.5e-6), 956 us (821); summing each half of a stage apart -4e-8, 137, 393, 1064 us.
+// (-2.5e-6), 956 us (821); summing each half of a stage apart -4e-8, 137, 393, 1064 us. bf16, 80 sequences of 16,384: d 64
+// -2.9e-8 (-2.4e-6), d 128 -3.3e-8 (-3.0e-6); the first and second case above take 2 and 4% longer for it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -215,10 +216,15 @@ __device__ __forceinline__ void products(const __nv_bfloat16*, const float (&p)[
         ldmatrix4_trans(chunk_at<__nv_bfloat16, D>(v, lane & 15, 2 * i + (lane >> 4)), b);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            mma_bf16(o[m][2 * i], hi[m], b[0], b[1]);
-            mma_bf16(o[m][2 * i + 1], hi[m], b[2], b[3]);
-            mma_bf16(o[m][2 * i], lo[m], b[0], b[1]);
-            mma_bf16(o[m][2 * i + 1], lo[m], b[2], b[3]);
+            float t[2][4] = {};                                  // the stage's sum, formed apart
+            mma_bf16(t[0], hi[m], b[0], b[1]);
+            mma_bf16(t[1], hi[m], b[2], b[3]);
+            mma_bf16(t[0], lo[m], b[0], b[1]);
+            mma_bf16(t[1], lo[m], b[2], b[3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[m][2 * i + j][e] += t[j][e];
         }
     }
 }

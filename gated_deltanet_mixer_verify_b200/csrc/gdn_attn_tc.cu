@@ -61,24 +61,35 @@ constexpr float kGrow = 16.f;                   // a score this far (base 2) abo
 constexpr int kFetch = 2;                       // warps that fetch, every other slot each
 constexpr int kMaskRing = 16;                   // more tiles than the ring holds, and the one in work
 
-// D columns of the head, NB blocks of 64 rows.
-template <int D, int NB>
+constexpr int kRows = 64;                       // rows of a row tile at most
+// Tiles whose products are added up in the matrix units. Those cut where they add, always towards zero, so a sum formed in them
+// all along loses with every tile (128 tiles, values of one: 2.0e-5 of it); sums of kFold tiles are therefore put together
+// by ordinary additions, which round, in tensor memory beside O: 2.2e-6, however long the sequence. It takes 3% of the second
+// case below (d 128: 2%, one sequence 1%; with folds of 8 tiles 4%, and no less with 32), and half the tensor memory at d 256, which is why a
+// tile has 64 rows: with 128 of them, 640 threads of 96 registers that spilled and two ring slots at d 256, calls of 96 and 128 rows took
+// us, 64 then 128 rows a tile: d 64 40 and 40, 47 and 50 (one sequence of 32K), 112 and 114, 112 and 124 (32 of 4096); d 128
+// 44 and 45, 49 and 53; 121 and 124, 118 and 133; d 256 63 and 66, 68 and 72; 165 and 171, 158 and 177.
+constexpr int kFold = 16;
+
+// D columns of the head.
+template <int D>
 struct Cfg {
-    static constexpr int kGroups = 2 * NB;                            // of 128 threads and 32 rows
+    static constexpr int kGroups = 2;                                 // of 128 threads and 32 rows
     static constexpr int kSoft = 128 * kGroups;                       // threads of the softmax
     static constexpr int kThreads = kSoft + 32 * (kFetch + 2);
     static constexpr int kKb = D / 64;                                // blocks of 64 columns of a K or V tile
     static constexpr int kMb = D > 128 ? D / 128 : 1;                 // M = 128 blocks of O^T
     static constexpr int kPer = kKb / kMb;                            // blocks of a ring slot: what one of them takes of V
     static constexpr int kSlot = kPer * kBlock;
-    static constexpr int kQ = 64 * NB * D * 2;
-    static constexpr int kP = NB * kBlock;                            // one term of P
+    static constexpr int kQ = kRows * D * 2;
+    static constexpr int kP = kBlock;                                 // one term of P
     // buffers of P: with two, a tile's weights are written while the product before still reads its own
-    static constexpr int kPb = NB == 1 && D <= 128 ? 2 : 1;
-    static constexpr int kSlots = D == 256 ? (NB == 1 ? 4 : 2) : D == 128 ? (NB == 1 ? 4 : 3) : 8;
+    static constexpr int kPb = D <= 128 ? 2 : 1;
+    static constexpr int kSlots = D == 64 ? 8 : 4;
     static constexpr int kBytes = kSlots * kSlot + kQ + 2 * kPb * kP + 1024;   // + alignment
-    static constexpr uint32_t kO = 2 * 64 * NB;                       // column of O^T behind two S^T
-    static constexpr uint32_t kCols = 64 * NB * (2 + kMb) <= 256 ? 256 : 512;
+    static constexpr uint32_t kO = 2 * kRows;                         // column of O^T behind two S^T
+    static constexpr uint32_t kSum = kO + kMb * kRows;                // and of the sums of the folds before
+    static constexpr uint32_t kCols = kSum + kMb * kRows <= 256 ? 256 : 512;
     static constexpr int kCpr = D / 8;                                // 16-byte chunks per row of Q
 };
 
@@ -208,13 +219,13 @@ __device__ __noinline__ void mend(const Args& x, int b, int h, int col, int firs
     }
 }
 
-// grid (C, row tiles of 64 NB). run: slots per copy, the largest power of two up to a tile that
+// grid (C, row tiles). run: slots per copy, the largest power of two up to a tile that
 // divides the page size.
-template <int D, int NB>
-__global__ void __launch_bounds__(Cfg<D, NB>::kThreads, 1)
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_constant__ CUtensorMap k_map,
                               const __grid_constant__ CUtensorMap v_map, int run) {
-    using G = Cfg<D, NB>;
+    using G = Cfg<D>;
     constexpr int kSoftWarps = G::kSoft / 32;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Bars bars;
@@ -308,7 +319,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 tc::fence_after_sync();
                 float s[32];
                 if (chunks > 0) {
-                    const uint32_t S = lanes + (g & 1) * (64 * NB) + 32 * wg;
+                    const uint32_t S = lanes + (g & 1) * kRows + 32 * wg;
                     tc::tmem_ld16x2(S, S + 16, *reinterpret_cast<float(*)[16]>(s), *reinterpret_cast<float(*)[16]>(s + 16));
                     if (x.c <= 0.f) {                            // c enters the exponents as |c|
 #pragma unroll
@@ -363,8 +374,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
 #pragma unroll
                         for (int r = 0; r < 32; ++r) l[r] *= s_k[wg][r];
 #pragma unroll 1
-                        for (int i = 0; i < G::kMb * 2; ++i) {
-                            const uint32_t O = lanes + G::kO + (i >> 1) * (64 * NB) + 32 * wg + (i & 1) * 16;
+                        for (int i = 0; i < G::kMb * (j > kFold ? 4 : 2); ++i) {   // O, and the sums of the folds before
+                            const uint32_t O = lanes + G::kO + (i >> 1) * kRows + 32 * wg + (i & 1) * 16;
                             float o[16];
                             tc::tmem_ld16(O, o);
 #pragma unroll
@@ -373,7 +384,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         }
                         tc::tmem_st_wait();
                     }
-                    unsigned char* P = ring + kPOff + g % G::kPb * (2 * G::kP) + (wg >> 1) * kBlock;
+                    unsigned char* P = ring + kPOff + g % G::kPb * (2 * G::kP);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {                // eight rows: one 16-byte chunk of each term
                         if (q >= 2 * chunks) break;
@@ -391,9 +402,25 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                             hi[e] = *reinterpret_cast<const uint32_t*>(&h2);
                             lo[e] = *reinterpret_cast<const uint32_t*>(&l2);
                         }
-                        const uint32_t to_chunk = tile_chunk(kTile, k, (wg & 1) * 4 + q);
+                        const uint32_t to_chunk = tile_chunk(kTile, k, wg * 4 + q);
                         *reinterpret_cast<uint4*>(P + to_chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(P + G::kP + to_chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    // A fold: O is added to the sums of the folds before, and the next product begins it anew. Here, where the
+                    // scores are used up (registers).
+                    if (j > 0 && j % kFold == 0) {
+                        if (!(fine = product_done(g - 1))) break;
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < G::kMb * 2; ++i) {
+                            const uint32_t O = lanes + G::kO + (i >> 1) * kRows + 32 * wg + (i & 1) * 16, sums = O + (G::kSum - G::kO);
+                            float o[16], t[16];
+                            tc::tmem_ld16x2(O, sums, o, t);
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) o[r] += j > kFold ? t[r] : 0.f;
+                            tc::tmem_st16_nowait(sums, o);
+                        }
+                        tc::tmem_st_wait();
                     }
                     tc::fence_proxy_async_smem();
                 } else if (j >= G::kPb && !(fine = product_done(g - G::kPb))) {
@@ -435,8 +462,11 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
 #pragma unroll 1
                 for (int i = 0; i < G::kMb * chunks; ++i) {
                     const int mb = i / chunks, q = i - mb * chunks, col = mb * 128 + k;
-                    float o[16];
-                    tc::tmem_ld16(lanes + G::kO + mb * (64 * NB) + 32 * wg + q * 16, o);
+                    const uint32_t O = lanes + G::kO + mb * kRows + 32 * wg + q * 16;
+                    float o[16], t[16];
+                    tc::tmem_ld16x2(O, O + (G::kSum - G::kO), o, t);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[r] += n > kFold ? t[r] : 0.f;
                     if (col >= D) continue;                      // d = 64: the upper lanes hold it twice
                     int64_t to[16];
                     float f[16];
@@ -572,8 +602,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         const uint64_t k_at = tc::desc_kmajor_sw128(ring_at + slot * G::kSlot);
 #pragma unroll
                         for (int i = 0; i < 4 * G::kPer; ++i)
-                            tc::mma_bf16_ss(tm + buf * (64 * NB), k_at + ((i >> 2) * kBlock + (i & 3) * 32) / 16,
-                                            q_at + ((mb * G::kPer + (i >> 2)) * (64 * NB * 128) + (i & 3) * 32) / 16, id_s, mb > 0 || i > 0);
+                            tc::mma_bf16_ss(tm + buf * kRows, k_at + ((i >> 2) * kBlock + (i & 3) * 32) / 16,
+                                            q_at + ((mb * G::kPer + (i >> 2)) * (kRows * 128) + (i & 3) * 32) / 16, id_s, mb > 0 || i > 0);
                         tc::mma_commit(&bars.kv_empty[slot]);
                         if (mb == G::kMb - 1) {
                             if (j == n - 1) tc::mma_commit(&bars.q_empty);
@@ -614,8 +644,8 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         // d = 64: the second 64 rows of M are the first again (a stride of 0)
                         const uint64_t v_at = tc::desc_mnmajor_sw128(ring_at + slot * G::kSlot, G::kPer == 2 ? kBlock : 0);
                         auto step = [&](int i) {                   // the leading term of P, then the other
-                            tc::mma_bf16_ss(tm + G::kO + mb * (64 * NB), v_at + (i & 7) * 2048 / 16, p_at + ((i >> 3) * G::kP + (i & 7) * 2048) / 16,
-                                            id_o, j > 0 || i > 0);
+                            tc::mma_bf16_ss(tm + G::kO + mb * kRows, v_at + (i & 7) * 2048 / 16, p_at + ((i >> 3) * G::kP + (i & 7) * 2048) / 16,
+                                            id_o, j % kFold != 0 || i > 0);
                         };
                         if (steps == kTile / 16) {
 #pragma unroll
@@ -663,7 +693,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (((int64_t)w.b * a.T + t) * a.Hq + (int64_t)w.h * share + head) * D + ch * 8;
 #pragma unroll 4
             for (; r < rows; r += kQRows) {
-                cp_async16(ring_at + kQOff + tile_chunk(64 * NB, r, ch), q, r < real);
+                cp_async16(ring_at + kQOff + tile_chunk(kRows, r, ch), q, r < real);
                 q += kQRows * D;
                 for (head += kQRows; head >= share; head -= share) q += (int64_t)(a.Hq - share) * D;   // the next token's
             }
@@ -732,27 +762,22 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     if (tid == 0 && s_lost && a.status_word) atomicOr(a.status_word, kStatusWaitTimeout);
 }
 
-template <int D, int NB>
+template <int D>
 cudaError_t launch(const Args& x, const Plan& p, cudaStream_t stream) {
-    using G = Cfg<D, NB>;
+    using G = Cfg<D>;
     static_assert(G::kBytes + 6144 <= 227 * 1024, "shared memory");
     const PagedCache& c = x.a.cache;
     const int run = std::min(kTile, c.page & -c.page);
     CUtensorMap maps[2];
-    cudaError_t e = ensure_smem_attr<gdn_paged_attention_tc_kernel<D, NB>>(G::kBytes);
+    cudaError_t e = ensure_smem_attr<gdn_paged_attention_tc_kernel<D>>(G::kBytes);
     for (int i = 0; i < 2 && e == cudaSuccess; ++i)
         e = tc::encode_tmap_paged(&maps[i], i ? c.v : c.k, D, x.a.Hk, c.page, c.num_pages, c.head_stride, c.slot_stride,
                                   c.page_stride, run);
     if (e != cudaSuccess) return e;
     Launch l(dim3(p.ctas, p.tiles), G::kThreads, G::kBytes, stream);
-    e = cudaLaunchKernelEx(&l.cfg, gdn_paged_attention_tc_kernel<D, NB>, x, maps[0], maps[1], run);
+    e = cudaLaunchKernelEx(&l.cfg, gdn_paged_attention_tc_kernel<D>, x, maps[0], maps[1], run);
     return e != cudaSuccess ? e : launch_join(x, p, stream);
 }
-template <int D>
-cudaError_t launch_rows(const Args& x, const Plan& p, cudaStream_t stream) {
-    return p.rows <= 64 ? launch<D, 1>(x, p, stream) : launch<D, 2>(x, p, stream);
-}
-
 }  // namespace
 
 bool tc_applies(const AttnArgs& a) {
@@ -771,14 +796,14 @@ Plan plan_tc(int sms, int rows) {
     Plan p;
     p.unit = kTile;
     p.extra = kExtra;
-    p.rows = std::min(rows, 128);
-    p.tiles = (rows + 127) / 128;
+    p.tiles = (rows + kRows - 1) / kRows;
+    p.rows = p.tiles == 1 ? rows : ((rows + p.tiles - 1) / p.tiles + 15) / 16 * 16;
     p.ctas = std::max(1, sms / p.tiles);
     return p;
 }
 
 cudaError_t launch_tc(const Args& x, const Plan& p, cudaStream_t stream) {
-    return x.a.d == 64 ? launch_rows<64>(x, p, stream) : x.a.d == 128 ? launch_rows<128>(x, p, stream) : launch_rows<256>(x, p, stream);
+    return x.a.d == 64 ? launch<64>(x, p, stream) : x.a.d == 128 ? launch<128>(x, p, stream) : launch<256>(x, p, stream);
 }
 
 }  // namespace attn

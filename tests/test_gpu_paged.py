@@ -613,6 +613,24 @@ def test_attention_long_fp32_sums_do_not_drift(gdn, d):
     assert float((o - 1).abs().max()) <= 2e-5 and abs(float((o - 1).mean())) <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page,T", [(16, 8), (20, 8), (20, 1)])
+def test_attention_long_bf16_sums_do_not_drift(gdn, d, page, T):
+    # As above, of a bf16 cache: 160 items of 65,536 positions (all over the same pages), so that a CTA holds whole ones, on the
+    # tensor-memory kernel (page 16) and the streaming one. A product of 16 positions cuts its sum by less than
+    # 2^-23 of it; 2 of them go into each sum of the streaming kernel, 256 into each of the other's, whose first half
+    # of growth counts half: 2^-22 and 2^-16 at most, however long the sequence; the additions that put those
+    # together round to either side (2^-24 each, 2^-22 in the mean is allowed). Sums formed in the units all along
+    # lose 8e-5 and 1e-5 here.
+    S, Hq, Hk = 65536, 12, 2
+    n = -(-S // page)
+    kc = torch.randn(n, page, Hk, d, generator=torch.Generator(device="cuda").manual_seed(d), device="cuda").to(BF)
+    q = torch.randn(80, T, Hq, d, device="cuda").to(BF)
+    table = torch.arange(n, dtype=torch.int32, device="cuda").repeat(80, 1)
+    o = gdn.paged_attention(q, kc, torch.ones_like(kc), table, _i32([S] * 80), out_dtype=F32).double()
+    assert abs(float((o - 1).mean())) <= (2.0 ** -16 if page == 16 else 2.0 ** -22) + 2.0 ** -22, float((o - 1).mean())
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_attention_many_items_for_each_cta(gdn, tables, d):
     rng = np.random.default_rng(d)
