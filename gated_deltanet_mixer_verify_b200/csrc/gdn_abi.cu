@@ -889,11 +889,10 @@ size_t gdn_paged_attention_workspace_bytes(const gdn_kv_shape* shape) {
                                                 shape->dtype == GDN_BF16);
 }
 
-gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
-                               const void* k_cache, const void* v_cache, const int32_t* block_table,
-                               const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
-                               size_t workspace_bytes, void* stream) {
-    const char* who = "gdn_paged_attention";
+static gdn_status paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                                  const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                  const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
+                                  size_t workspace_bytes, uint32_t polls, void* stream, const char* who) {
     gdn_status st = check_attention(shape, who);
     if (st == GDN_OK) st = check_kv(shape, 16, who);
     if (st == GDN_OK) st = check_table(shape, who);
@@ -943,7 +942,26 @@ gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t w
     a.lse = lse;
     a.workspace = workspace;
     a.status_word = shape->status_word;
+    a.polls = polls;
     return launched(gdn::launch_paged_attention(a, static_cast<cudaStream_t>(stream)), who);
+}
+
+gdn_status gdn_paged_attention(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                               const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    return paged_attention(shape, scale, window, q, k_cache, v_cache, block_table, kv_len, q_len, o, lse, workspace, workspace_bytes, 0,
+                           stream, "gdn_paged_attention");
+}
+
+gdn_status gdn_selftest_attention_wait(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                                       const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                       const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
+                                       size_t workspace_bytes, uint32_t polls, void* stream) {
+    const char* who = "gdn_selftest_attention_wait";
+    if (polls == 0 || polls > (1u << 20)) return fail(GDN_ERR_INVALID_ARG, "%s: polls must be 1..2^20", who);
+    return paged_attention(shape, scale, window, q, k_cache, v_cache, block_table, kv_len, q_len, o, lse, workspace, workspace_bytes, polls,
+                           stream, who);
 }
 
 gdn_status gdn_selftest_bounded_wait(int32_t* status_word, uint32_t polls, void* stream) {

@@ -634,6 +634,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream) {
     x.parts = parts_at(a.workspace, p, a.d);
     x.rows = p.rows;
     x.c = a.scale * kLog2e;
+    x.polls = a.polls ? a.polls : kMaxPolls;
     if (on_tc) return launch_tc(x, p, stream);
     if (a.bf16)
         return a.d == 64 ? launch_rows<__nv_bfloat16, 64>(x, p, stream)

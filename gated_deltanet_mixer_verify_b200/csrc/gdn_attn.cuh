@@ -68,7 +68,7 @@ struct Parts {
     int64_t* units;   // [2], the second unused
     Lead* lead;       // [C]
     float* o;         // [tiles][C][2][rows][D]
-    float* m;         // [tiles][C][2][rows], base-2 exponents
+    float* m;         // [tiles][C][2][rows], base-2 exponents (NaN: the CTA gave up)
     float* l;
 };
 inline size_t parts_bytes(const Plan& p, int D) {
@@ -90,7 +90,9 @@ struct Args {
     Parts parts;
     int rows;
     float c;        // scale log2(e): the softmax runs on base-2 exponents
+    uint32_t polls; // after which a wait gives up
 };
+constexpr uint32_t kMaxPolls = 1u << 22;
 
 // What a sequence asks for. rows == 0: nothing (also where its counts cannot be).
 struct Seq {

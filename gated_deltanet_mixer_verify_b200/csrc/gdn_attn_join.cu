@@ -24,6 +24,7 @@ constexpr int kMaxLeads = kMaxSms * 3;      // CTAs per row tile at most
 template <int N>
 struct Sum {
     float m, l, o[N];
+    bool gone;      // a part's CTA gave up
 };
 
 // 2^x, but never 0: a part's sums may be infinite (a value was), and stay so however small its weight. A part this far
@@ -56,7 +57,10 @@ __device__ __forceinline__ void add_parts(const Args& x, const Deal& deal, int C
         }
         float top = s.m;
 #pragma unroll
-        for (int f = 0; f < F; ++f) top = fmaxf(top, pm[f]);
+        for (int f = 0; f < F; ++f) {
+            s.gone |= isnan(pm[f]);
+            top = fmaxf(top, pm[f]);
+        }
         const float use = top == -INFINITY ? 0.f : top;
         const float k = weight(s.m - use);
         s.l *= k;
@@ -114,11 +118,13 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
         Sum<N> s;
         s.m = -INFINITY;
         s.l = 0.f;
+        s.gone = false;
 #pragma unroll
         for (int e = 0; e < N; ++e) s.o[e] = 0.f;
         add_parts<D>(x, deal, C, tile, r, it, it.c0 + (together ? warp : 0), together ? kWarps : 1, lane, s);
         const int64_t out = ((int64_t)it.b * a.T + t) * a.Hq + (int64_t)it.h * G + (row - t * G);
         if (!together) {
+            if (s.gone) continue;
             const float inv = 1.f / s.l;                         // (l = 0: o = 0)
 #pragma unroll
             for (int e = 0; e < N; ++e) store_o(a, out * D + e * 32 + lane, s.l == 0.f ? 0.f : s.o[e] * inv);
@@ -129,13 +135,18 @@ __global__ void __launch_bounds__(kThreads) gdn_paged_attention_join_kernel(cons
 #pragma unroll
         for (int e = 0; e < N; ++e) s_o[warp][e * 32 + lane] = s.o[e];
         if (lane == 0) {
-            s_m[warp] = s.m;
+            s_m[warp] = s.gone ? NAN : s.m;
             s_l[warp] = s.l;
         }
         __syncthreads();
         float top = -INFINITY;
+        bool gone = false;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
+        for (int w = 0; w < kWarps; ++w) {
+            gone |= isnan(s_m[w]);
+            top = fmaxf(top, s_m[w]);
+        }
+        if (gone) continue;                        // (the only row)
         const float use = top == -INFINITY ? 0.f : top;
         float sum = 0.f, f[kWarps];
 #pragma unroll

@@ -21,7 +21,8 @@
 // the products, one that fetches queries and looks over the values at the ends of what the rows see.
 // The order of products, and of the ring, is K 0, K 1, V 0, K 2, V 1, ...: scores of the next tile
 // are formed before the values of this one are needed, so a block is used up as it lands, the
-// softmax runs while values land, and the whole ring is copies in flight. Every wait is bounded.
+// softmax runs while values land, and the whole ring is copies in flight. Every wait is bounded: a CTA that gives up
+// writes nothing of the items it is at, and what was split with it is not joined.
 //
 // Bound: HBM and the chain within a tile together. A tile of 128 positions (d 256) is 128 KB, 5,700 cycles of
 // an SM's share of HBM; its 16 score and 32 output products of M 128, N 48, K 16 take 2,300 (48 each,
@@ -56,7 +57,6 @@ constexpr int kTile = 128;                      // positions per tile, and per u
 // 32K positions (d 256, 48 rows) 52.3, 45.8, 47.5; 32 sequences of 100 .. 8192 117.9, 113.5, 112.9; 128 of 100 .. 512 97.7, 96.5, 96.2.
 constexpr int kExtra = 3;
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
-constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
 constexpr int kFetch = 2;                       // warps that fetch, every other slot each
 constexpr int kMaskRing = 16;                   // more tiles than the ring holds, and the one in work
@@ -118,12 +118,12 @@ __device__ __forceinline__ __nv_bfloat162 taint(uint32_t w, __nv_bfloat162 sum) 
 }
 
 // Waits of a whole warp, its lanes agreeing, that give up when the CTA has been given up, or after
-// kMaxPolls polls, and then give the CTA up. First on a count in shared memory that one thread raises:
+// `polls` polls, and then give the CTA up. First on a count in shared memory that one thread raises:
 __device__ __forceinline__ void set_count(uint32_t* count, uint32_t n) {
     asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
 }
-__device__ __forceinline__ bool await_count(uint32_t* count, uint32_t want, volatile int* lost) {
-    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+__device__ __forceinline__ bool await_count(uint32_t* count, uint32_t want, uint32_t polls, volatile int* lost) {
+    for (uint32_t i = 0; i < polls; ++i) {
         uint32_t n;
         asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(n) : "r"(smem_u32(count)) : "memory");
         if ((int32_t)(n - want) >= 0) return true;
@@ -134,8 +134,8 @@ __device__ __forceinline__ bool await_count(uint32_t* count, uint32_t want, vola
     return false;
 }
 // and on a barrier:
-__device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, volatile int* lost) {
-    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+__device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* lost) {
+    for (uint32_t i = 0; i < polls; ++i) {
         if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(kFull, *lost)) return false;
     }
@@ -288,6 +288,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     const int share = a.Hq / a.Hk, row0 = mtile * x.rows, all_rows = share * a.T;
     const int rows = min(x.rows, all_rows - row0);
     Walk<kTile, kExtra> w(at);
+    uint32_t issued = 0;                             // slots of the ring, as far as a fetching warp has come
 
     if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax and outputs
@@ -298,10 +299,12 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float cs = x.c == 0.f ? 1.f : fabsf(x.c);
         // the product of tile t is done
-        auto product_done = [&](uint32_t t) { return await_warp(&bars.pv_done[t & 1], (t >> 1) & 1, &s_lost); };
+        auto product_done = [&](uint32_t t) { return await_warp(&bars.pv_done[t & 1], (t >> 1) & 1, x.polls, &s_lost); };
         // Tiles done by this CTA. Its first item begins with a tile -1, worked without waiting for anything and
         // forgotten: while the first keys are on their way, it brings the instructions in (4,000 cycles of misses).
         uint32_t g = ~0u;
+        // The four warps of a group meet at barriers that nothing bounds. So one whose wait has given up goes on without
+        // waiting, to the vote at the item's end, where all four leave or none.
         bool fine = true;
         int item = 0;                                            // counted from 1
         float l[32];
@@ -315,7 +318,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
 #pragma unroll
                     for (int r = 0; r < 32; ++r) l[r] = 0.f;
                 }
-                if (j >= 0 && !(fine = await_warp(&bars.s_full[g & 1], (g >> 1) & 1, &s_lost))) break;
+                if (j >= 0) fine = fine && await_warp(&bars.s_full[g & 1], (g >> 1) & 1, x.polls, &s_lost);
                 tc::fence_after_sync();
                 float s[32];
                 if (chunks > 0) {
@@ -367,9 +370,9 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         named_barrier_sync(bar, 128);
                     }
                     // the product that last read this buffer of P; and O is rescaled behind the one before
-                    if (j >= G::kPb && !(fine = product_done(g - G::kPb))) break;
+                    if (j >= G::kPb) fine = fine && product_done(g - G::kPb);
                     if (move && j > 0) {
-                        if (!(fine = product_done(g - 1))) break;
+                        fine = fine && product_done(g - 1);
                         tc::fence_after_sync();
 #pragma unroll
                         for (int r = 0; r < 32; ++r) l[r] *= s_k[wg][r];
@@ -409,7 +412,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     // A fold: O is added to the sums of the folds before, and the next product begins it anew. Here, where the
                     // scores are used up (registers).
                     if (j > 0 && j % kFold == 0) {
-                        if (!(fine = product_done(g - 1))) break;
+                        fine = fine && product_done(g - 1);
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int i = 0; i < G::kMb * 2; ++i) {
@@ -423,18 +426,20 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                         tc::tmem_st_wait();
                     }
                     tc::fence_proxy_async_smem();
-                } else if (j >= G::kPb && !(fine = product_done(g - G::kPb))) {
-                    break;
+                } else if (j >= G::kPb) {
+                    fine = fine && product_done(g - G::kPb);
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0 && j >= 0) mbar_arrive(&bars.p_full[g & 1]);
+                if (lane == 0 && j >= 0 && fine) mbar_arrive(&bars.p_full[g & 1]);
             }
-            if (!fine) break;
             // the sums, and where the rows go
+            if (chunks > 0) s_part[wg][warp & 3][lane] = reduce32<false>(l, lane);
+            fine = fine && product_done(g - 1);
+            if (chunks > 0) fine = !any128(bar, !fine);
+            if (!fine) break;
+            tc::fence_after_sync();
             if (chunks > 0) {
-                s_part[wg][warp & 3][lane] = reduce32<false>(l, lane);
-                named_barrier_sync(bar, 128);
                 if (k < 32) {
                     const int row = my_row0 + k, t = row / share;
                     const float sum = (s_part[wg][0][k] + s_part[wg][1][k]) + (s_part[wg][2][k] + s_part[wg][3][k]);
@@ -445,7 +450,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                             if (a.lse) a.lse[to] = (s_use[wg][k] + log2f(sum)) * kLn2;
                         } else {
                             to = (((int64_t)mtile * C + c) * 2 + w.slot) * x.rows + 32 * wg + k;
-                            x.parts.m[to] = s_m[wg][k];
+                            x.parts.m[to] = isnan(s_m[wg][k]) ? -INFINITY : s_m[wg][k];   // (sum is NaN then)
                             x.parts.l[to] = sum;
                         }
                     }
@@ -453,10 +458,6 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                     s_k[wg][k] = isnan(sum) ? sum : !w.whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
                 }
                 named_barrier_sync(bar, 128);
-            }
-            if (!(fine = product_done(g - 1))) break;
-            tc::fence_after_sync();
-            if (chunks > 0) {
                 const bool repair = s_not_numbers == item;
                 const int end = min(w.s.kv, first + n * kTile);
 #pragma unroll 1
@@ -505,7 +506,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
         const uint32_t fw = warp - kSoftWarps;
         const int page = a.cache.page, runs = kTile / run;
         const int r = lane % runs, blk = lane / runs;            // this lane's run of the tile, and its block of a slot
-        uint32_t issued = 0, g = 0;                  // slots of the ring, tiles
+        uint32_t g = 0;                              // tiles
         bool fine = true;
         while (fine && w.next(x)) {
             if (row0 / share >= w.s.rows) continue;
@@ -532,7 +533,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 for (int i = 0; i < G::kMb; ++i, ++issued) {
                     if (issued % kFetch != fw) continue;
                     const uint32_t slot = issued % G::kSlots, round = issued / G::kSlots;
-                    if (!await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, &s_lost)) return false;
+                    if (!await_warp(&bars.kv_empty[slot], (round & 1) ^ 1, x.polls, &s_lost)) return false;
                     if (keys && i == 0) {
                         // the tile's positions that are there, 32 to a word
 #pragma unroll
@@ -567,12 +568,6 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 id_next = look_up(j + 2);
             }
         }
-        if (!fine) {
-            // given up: let the copies in flight land before the shared memory goes
-            for (uint32_t s = issued > G::kSlots ? issued - G::kSlots : 0; s < issued; ++s)
-                if (s % kFetch == fw)
-                for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.kv_full[s % G::kSlots], (s / G::kSlots) & 1); ++i) {}
-        }
     } else if (warp == kSoftWarps + kFetch) {
         // ---------------------------------------------------------------- products
         // The whole warp walks and waits alike and one elected lane issues: what the products take (addresses,
@@ -590,13 +585,13 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             if (row0 / share >= w.s.rows) continue;
             const Sight see(a, w.s, row0, row0 + rows, share);
             const int n = __shfl_sync(kFull, w.i1 - w.i0, 0), first = __shfl_sync(kFull, w.s.first + w.i0 * kTile, 0);
-            if (!(fine = await_warp(&bars.q_full, items & 1, &s_lost))) break;
+            if (!(fine = await_warp(&bars.q_full, items & 1, x.polls, &s_lost))) break;
             // S^T = K Q^T of tile j: into the buffer that tile j - 2's reader has left
             auto score = [&](int j) -> bool {
                 const uint32_t buf = (g + j) & 1;
 #pragma unroll
                 for (int mb = 0; mb < G::kMb; ++mb) {
-                    if (!await_warp(&bars.kv_full[slot], phase, &s_lost)) return false;
+                    if (!await_warp(&bars.kv_full[slot], phase, x.polls, &s_lost)) return false;
                     tc::fence_after_sync();
                     if (elect_one()) {
                         const uint64_t k_at = tc::desc_kmajor_sw128(ring_at + slot * G::kSlot);
@@ -620,25 +615,25 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             for (int j = 0; j < n; ++j) {
                 if (j + 1 < n && !(fine = score(j + 1))) break;
                 // O^T += V^T P^T
-                if (!(fine = await_warp(&bars.p_full[(g + j) & 1], ((g + j) >> 1) & 1, &s_lost))) break;
-                if (j == 0 && items > 0 && !(fine = await_warp(&bars.o_free, (items - 1) & 1, &s_lost))) break;
+                if (!(fine = await_warp(&bars.p_full[(g + j) & 1], ((g + j) >> 1) & 1, x.polls, &s_lost))) break;
+                if (j == 0 && items > 0 && !(fine = await_warp(&bars.o_free, (items - 1) & 1, x.polls, &s_lost))) break;
                 if (see.partial(first + j * kTile, kTile)) {
                     uint32_t sl = slot, ph = phase;
                     for (int mb = 0; mb < G::kMb && fine; ++mb) {
-                        fine = await_warp(&bars.kv_full[sl], ph, &s_lost);
+                        fine = await_warp(&bars.kv_full[sl], ph, x.polls, &s_lost);
                         if (++sl == G::kSlots) sl = 0, ph ^= 1;
                     }
                     if (!fine) break;
                     ++looked;
                     if (lane == 0) set_count(&s_ask, looked);
-                    if (!(fine = __all_sync(kFull, await_count(&s_looked, looked, &s_lost)))) break;
+                    if (!(fine = __all_sync(kFull, await_count(&s_looked, looked, x.polls, &s_lost)))) break;
                 }
                 const uint64_t p_at = p_base + (g + j) % G::kPb * (2 * G::kP) / 16;
                 // steps of 16 positions; those behind the sequence are left out, and what is there with them
                 const int steps = __shfl_sync(kFull, min(kTile, max(w.s.kv - first - j * kTile, 1) + 15) / 16, 0);
 #pragma unroll
                 for (int mb = 0; mb < G::kMb; ++mb) {
-                    if (!(fine = await_warp(&bars.kv_full[slot], phase, &s_lost))) break;
+                    if (!(fine = await_warp(&bars.kv_full[slot], phase, x.polls, &s_lost))) break;
                     tc::fence_after_sync();
                     if (elect_one()) {
                         // d = 64: the second 64 rows of M are the first again (a stride of 0)
@@ -669,12 +664,6 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             g += n;
             ++items;
         }
-        if (!fine && elect_one()) {
-            // given up: let the products in flight end before the tensor memory goes
-            tc::mma_commit(&bars.drain);
-            for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.drain, 0); ++i) {}
-        }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------------- queries, and values at the ends
         constexpr int kAtOnce = 8;                               // reads of values in flight, 16 bytes each
@@ -686,7 +675,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
             do {
                 if (!w.next(x)) return false;
             } while (row0 / share >= w.s.rows);
-            if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, &s_lost))) return false;
+            if (items > 0 && !(fine = await_warp(&bars.q_empty, (items - 1) & 1, x.polls, &s_lost))) return false;
             // rows behind the sequence's last are zeros, whatever q holds there: the votes on the maxima are taken among all
             const int ch = lane % G::kCpr, real = share * w.s.rows - row0;
             int r = lane / G::kCpr, t = (row0 + r) / share, head = row0 + r - t * share;
@@ -716,7 +705,7 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
                 if (j == n - 1) more = next_item();
                 const int pos = first + j * kTile;
                 if (!fine || !see.partial(pos, kTile)) continue;
-                if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, &s_lost)))) break;
+                if (!(fine = __all_sync(kFull, await_count(&s_ask, ++looked, x.polls, &s_lost)))) break;
                 const uint32_t v_slot = slot0 + (j < n - 1 ? 2 * j + 2 : 2 * n - 1) * G::kMb;   // V's first
                 // rows 0 .. low - 1 and high .. stop - 1 of the tile; behind them TMA has left zeros, or the product stops
                 const int behind = max(kv - pos, 0), stop = min(kTile, min((behind + run - 1) / run * run, (behind + 15) / 16 * 16));
@@ -758,6 +747,21 @@ gdn_paged_attention_tc_kernel(const __grid_constant__ Args x, const __grid_const
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    if (s_lost) {
+        // Given up: the copies in flight land, and the products end, before the memory goes; and the join is told (a
+        // maximum of NaN) that there is no part of this CTA's.
+        if (warp >= kSoftWarps && warp < kSoftWarps + kFetch)
+            for (uint32_t s = issued > G::kSlots ? issued - G::kSlots : 0; s < issued; ++s)
+                if (s % kFetch == warp - kSoftWarps)
+                    for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.kv_full[s % G::kSlots], (s / G::kSlots) & 1); ++i) {}
+        if (warp == kSoftWarps + kFetch) {
+            if (elect_one()) tc::mma_commit(&bars.drain);
+            for (uint32_t i = 0; i < kMaxPolls && !mbar_try_wait(&bars.drain, 0); ++i) {}
+            __syncwarp();
+        }
+        if (C > 1)
+            for (int i = tid; i < 2 * x.rows; i += G::kThreads) x.parts.m[((size_t)mtile * C + c) * 2 * x.rows + i] = NAN;
+    }
     if (warp == kSoftWarps + kFetch) tc::tmem_dealloc(tmem, G::kCols);
     if (tid == 0 && s_lost && a.status_word) atomicOr(a.status_word, kStatusWaitTimeout);
 }

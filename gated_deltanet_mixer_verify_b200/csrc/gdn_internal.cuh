@@ -237,6 +237,7 @@ struct AttnArgs {
     float* lse;                  // or nullptr
     void* workspace;
     int32_t* status_word;
+    uint32_t polls;              // limit of the kernels' waits, 0: their own
 };
 size_t paged_attention_workspace_bytes(int B, int T, int Hq, int Hk, int d, bool bf16);
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t stream);

@@ -89,12 +89,13 @@ def _load():
     lib.gdn_kv_plan.argtypes = [_VP] * 16
     lib.gdn_rope_append.argtypes = [_VP] * 16
     lib.gdn_paged_attention.argtypes = ([_VP, ctypes.c_float, ctypes.c_int32] + [_VP] * 9 + [ctypes.c_size_t, _VP])
+    lib.gdn_selftest_attention_wait.argtypes = lib.gdn_paged_attention.argtypes[:-1] + [ctypes.c_uint32, _VP]
     lib.gdn_paged_attention_workspace_bytes.argtypes = [_VP]
     lib.gdn_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     for fn in ("gdn_kv_plan", "gdn_rope_append", "gdn_paged_attention", "gdn_verify_step", "gdn_commit", "gdn_decode_step", "gdn_commit_and_verify", "gdn_chunk_prefill",
                "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_prepare", "gdn_chunk_prefill_scan",
                "gdn_short_conv", "gdn_verify_step_gated", "gdn_gated_rmsnorm", "gdn_accept",
-               "gdn_selftest_bounded_wait", "gdn_selftest_accept_wait"):
+               "gdn_selftest_bounded_wait", "gdn_selftest_accept_wait", "gdn_selftest_attention_wait"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.gdn_stash_bytes.argtypes = [S]
     lib.gdn_stash_bytes.restype = ctypes.c_size_t
@@ -720,3 +721,17 @@ def paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=
     if rc:
         _check(rc)
     return o
+
+
+def selftest_attention_wait(q, k_cache, v_cache, block_table, kv_len, o, lse, workspace, status_word, polls=64, stream=None):
+    """:func:`paged_attention` whose waits give up after `polls` polls: where one does, the wait-timeout bit (2) is ORed
+    into status_word (device int32) and the rows concerned are not written to o and lse."""
+    B, T, H_q, d = q.shape
+    dtype, dev = q.dtype, q.get_device()
+    page, pages, page_stride, slot_stride, head_stride, p_kc, p_vc = _cache(k_cache, v_cache, k_cache.shape[2], d, dtype, dev)
+    max_pages = block_table.shape[1]
+    p_q, *args, status = _pointers(_ATTENTION[dtype, o.dtype], dev, (B, T, H_q, d, max_pages, 1), q, block_table, kv_len, None, o, lse, status_word)
+    shape = _pack_kv_shape(B, T, H_q, k_cache.shape[2], d, _dtype_code(dtype), _dtype_code(o.dtype), page, pages, max_pages, page_stride,
+                           slot_stride, head_stride, status or 0)
+    _check(_load().gdn_selftest_attention_wait(shape, d ** -0.5, 0, p_q, p_kc, p_vc, *args, _ptr(workspace), _nbytes(workspace), polls,
+                                               _raw_stream(stream, dev)))

@@ -68,7 +68,7 @@ extern "C" {
 #endif
 
 /* Additions that change no struct and no call keep the number: a caller that needs gdn_kv_plan,
- * gdn_rope_append or gdn_paged_attention looks the symbol up (they came after 10 was set).
+ * gdn_rope_append, gdn_paged_attention or gdn_selftest_attention_wait looks the symbol up (they came after 10 was set).
  * 10: gdn_selftest_accept_wait; 9: gdn_last_verify_kernel; 8: gdn_shape.launch_flags (GDN_LAUNCH_PDL); 7: prefill in pieces (gdn_chunk_prefill_pieces);
  * 6: gdn_accept; 5: gated norm; 4: gdn_short_conv; 3: commit-and-verify */
 #define GDN_ABI_VERSION 10
@@ -522,6 +522,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  *   Rows t >= q_len[b] are left as they were in o and lse, and what q holds there changes nothing. A sequence with kv_len[b] outside
  *   0..max_pages * page_size or q_len[b] outside 0..T writes nothing (GDN_STATUS_BAD_LENGTH).
  *   Positions on a page id outside the pool are not seen (GDN_STATUS_BAD_PAGE).
+ *   GDN_STATUS_WAIT_TIMEOUT: a CTA gave up; the rows of the sequences and key heads it was at were not written.
  *   workspace  gdn_paged_attention_workspace_bytes, 16-byte aligned, contents irrelevant on entry;
  *              calls that may overlap on the GPU need one each (two captured graphs included).
  * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products
@@ -572,6 +573,18 @@ gdn_status gdn_selftest_bounded_wait(int32_t* status_word, uint32_t polls, void*
  * usable. Nothing faults, traps or hangs.
  */
 gdn_status gdn_selftest_accept_wait(int32_t* status_word, int32_t* next_token, uint32_t polls, void* stream);
+
+/*
+ * gdn_selftest_attention_wait -- test hook for the waits of gdn_paged_attention's tensor-memory kernel, the one that
+ * takes bf16 caches with many rows per key head: the same call, whose waits give up after `polls` polls
+ * (1..2^20). Where one does, its CTA waits for its own copies and products in flight, ORs GDN_STATUS_WAIT_TIMEOUT into the shape's
+ * status word and returns; rows that lack a part of its are not written, all others are as ever. The context
+ * stays usable. Nothing faults, traps or hangs.
+ */
+gdn_status gdn_selftest_attention_wait(const gdn_kv_shape* shape, float scale, int32_t window, const void* q,
+                                       const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                       const int32_t* kv_len, const int32_t* q_len, void* o, float* lse, void* workspace,
+                                       size_t workspace_bytes, uint32_t polls, void* stream);
 
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status status);

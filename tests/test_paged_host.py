@@ -126,6 +126,14 @@ def test_attention_refusals(gdn):
     assert call(_shape(gdn, B=0), q=None) == 0
 
 
+def test_attention_selftest_refusals(gdn):
+    at = [FAKE * (i + 1) for i in range(9)]
+    call = lambda polls, *p: gdn.lib().gdn_selftest_attention_wait(_shape(gdn), 0.1, 0, *(p or at), 1 << 40, polls, None)  # noqa: E731
+    for polls in (0, (1 << 20) + 1):
+        assert call(polls) == INVALID and "polls" in _err(gdn)
+    assert call(16, None, *at[1:]) == INVALID and _err(gdn).startswith("gdn_selftest_attention_wait: q is NULL")
+
+
 def test_binding_refusals(gdn):
     # raised before any pointer is taken, so CPU tensors suffice
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
