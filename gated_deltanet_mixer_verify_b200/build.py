@@ -5,11 +5,14 @@
 Each csrc/*.cu file is compiled by nvcc (in parallel) and linked into the package
 directory, next to this file, with the CUDA runtime linked statically so that the
 library loads on machines without a GPU. _binding.so beside it (csrc/binding.cpp, by the host
-compiler, against PyTorch's headers) is the native half of gdn.py's argument checks.
+compiler, against PyTorch's headers) is the native half of gdn.py's argument checks. It is built after
+the library, and left out where PyTorch or Python's headers are missing: users of the C ABI need nvcc alone.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -76,9 +79,28 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
+def binding_lacks() -> str:
+    """What _binding.so needs and this machine does not have ("" if nothing)."""
+    if importlib.util.find_spec("torch") is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return "" if shutil.which(CXX) else "a host compiler (%s)" % CXX
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libgdn.so (and _binding.so) if any source is newer than it; return its path."""
-    build_binding(force)
+    lib = build_library(force, verbose)
+    lacks = binding_lacks()
+    if lacks:
+        print("_binding.so not built, no %s: libgdn.so serves its C ABI; the Python binding needs both" % lacks, file=sys.stderr)
+    else:
+        build_binding(force)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link libgdn.so, with nvcc alone; return its path."""
     if not force and not needs_build():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
