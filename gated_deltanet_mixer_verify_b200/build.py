@@ -59,16 +59,32 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def binding_versions() -> str:
+    """What _binding.so is built against. It reads PyTorch's C++ objects, so it serves no other."""
+    import torch
+    return "PyTorch %s, %s, C++ ABI %d" % (torch.__version__, sysconfig.get_config_var("SOABI"), torch._C._GLIBCXX_USE_CXX11_ABI)
+
+
+def binding_is_stale() -> bool:
+    """Whether _binding.so is missing, older than its source, or built against other versions (the stamp beside it)."""
+    try:
+        with open(BINDING + ".for") as f:
+            versions = f.read()
+        built = os.path.getmtime(BINDING)
+    except OSError:
+        return True
+    return versions != binding_versions() or built < max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.abspath(__file__)))
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile _binding.so if its source is newer than it; return its path."""
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(
-            os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.abspath(__file__))):
+    """Compile _binding.so if it is stale; return its path."""
+    if not force and not binding_is_stale():
         return BINDING
     import torch
     base = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp.%d" % os.getpid()
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-DGDN_BUILT_FOR=\"%s\"" % binding_versions(), "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
            "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), BINDING_SRC, "-o", tmp,
            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
@@ -76,6 +92,8 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("%s failed on %s:\n%s%s" % (CXX, BINDING_SRC, r.stdout, r.stderr))
     os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(binding_versions())
     return BINDING
 
 

@@ -133,4 +133,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+// built_for: the versions of PyTorch and Python whose headers this was compiled with; the importer compares them.
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* m = PyModule_Create(&kModule);
+    if (m && PyModule_AddStringConstant(m, "built_for", GDN_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

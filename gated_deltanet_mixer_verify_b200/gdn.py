@@ -122,11 +122,15 @@ def _native():
     """The native half of the argument checks (csrc/binding.cpp)."""
     global _native_module
     if _native_module is None:
+        from .build import binding_versions
+        how = "run `python -m gated_deltanet_mixer_verify_b200.build` (or __graft_entry__.build())"
         try:
             from . import _binding
         except ImportError as e:
-            raise ImportError("_binding.so not built: run `python -m gated_deltanet_mixer_verify_b200.build` "
-                              "(or __graft_entry__.build())") from e
+            raise ImportError("_binding.so not built, or for other versions (%s): %s" % (e, how)) from e
+        built_for = getattr(_binding, "built_for", "other versions")
+        if built_for != binding_versions():            # it would read another PyTorch's objects by this one's layout
+            raise ImportError("_binding.so was built for %s, not for %s: %s" % (built_for, binding_versions(), how))
         _native_module = _binding
     return _native_module
 

@@ -40,3 +40,14 @@ def test_the_library_comes_first(monkeypatch):
     with pytest.raises(RuntimeError, match="the compiler's message"):
         gbuild.build()
     assert done == ["library", "binding"]
+
+
+def test_a_binding_built_for_other_versions_is_built_anew_and_never_used(monkeypatch):
+    gbuild.build()
+    from gated_deltanet_mixer_verify_b200 import gdn
+    assert not gbuild.binding_is_stale() and gdn._native().built_for == gbuild.binding_versions()
+    monkeypatch.setattr(gbuild, "binding_versions", lambda: "PyTorch 99")
+    assert gbuild.binding_is_stale()
+    monkeypatch.setattr(gdn, "_native_module", None)
+    with pytest.raises(ImportError, match="built for PyTorch .* not for PyTorch 99.*gated_deltanet_mixer_verify_b200.build"):
+        gdn._native()
