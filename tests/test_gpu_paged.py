@@ -715,6 +715,40 @@ def test_attention_streams_graphs_and_repeats(gdn, tables):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("T,Hq,d,page", [(8, 12, 64, 16), (8, 12, 128, 16), (8, 12, 256, 16), (16, 12, 64, 16), (16, 12, 256, 16), (8, 12, 128, 20), (1, 4, 256, 16)])
+def test_attention_maxima_that_grow_along_a_sequence(gdn, T, Hq, d, page):
+    # Rows whose best score so far is left behind by 2^16 and more, again and again, in tiles far into an item, each row
+    # at places of its own; a CTA holds some twenty tiles of an item. Scores of up to 80 (1.1 times that in sums of their
+    # terms' sizes, A): 16 steps of a product cut 2^-23 each, so a weight is off by 2e-6 A, o by twice that and the
+    # 4e-5 of other scores, of max|v|. A row one of whose keys is 40 ahead of all others is that key's value.
+    B, Hk = 64, 2
+    rng = np.random.default_rng([T, d, page])
+    lens = rng.integers(2500, 3300, B).tolist()
+    x = _attn_case(T, Hq, Hk, d, BF, page, lens, seed=d + T)
+    q = _f64(x["q"])
+    final = {}
+    for b, n in enumerate(lens):
+        for i, pos in enumerate(np.sort(rng.choice(n - T, 8, replace=False))):
+            t, h = int(rng.integers(T)), int(rng.integers(Hq))
+            score = 12.0 + 9.0 * i if (b % 4) else 80.0 - 8.0 * i           # growing, or the greatest first
+            key = q[b, t, h] * score * d ** 0.5 / (q[b, t, h] ** 2).sum()
+            x["kc"][x["table"][b, pos // page], pos % page, h * Hk // Hq] = torch.as_tensor(key).to(BF).cuda()
+        t, h, pos = int(rng.integers(T)), int(rng.integers(Hq)), int(rng.integers(n // 2, n - T))
+        key = q[b, t, h] * 140.0 * d ** 0.5 / (q[b, t, h] ** 2).sum()
+        if b % 2:
+            x["kc"][x["table"][b, pos // page], pos % page, h * Hk // Hq] = torch.as_tensor(key).to(BF).cuda()
+            final[b] = (t, h, pos)
+    o, lse = _run_attn(gdn, x, check=False)
+    for b, (t, h, pos) in final.items():
+        assert torch.equal(o[b, t, h], x["vc"][x["table"][b, pos // page], pos % page, h * Hk // Hq]), b
+    few = [0, 1, 2, 4, 7, 62]
+    r, rl, _ = paged.paged_attention(q[few], _f64(x["kc"]), _f64(x["vc"]), x["table"][few], x["kv"][few], None, None, 0)
+    top = float(np.nanmax(np.abs(_f64(x["vc"]))))
+    A = 160.0
+    assert (np.abs(_f64(o)[few] - r) <= (2 * 2e-6 * A + 4e-5) * top + 2.0 ** -8 * np.abs(r)).all()
+    assert (np.abs(_f64(lse)[few] - rl) <= 2e-6 * A + 2e-5 + 2.0 ** -22 * np.abs(rl)).all()
+
+
 def test_attention_kernel_choice(gdn):
     # each branch of the rule, on both of its sides
     def name(B, T, Hq, Hk, d, dt, page, capacity):
@@ -738,6 +772,65 @@ def test_attention_empty_batch(gdn):
 
 
 # ------------------------------------------------------------------------------ together
+
+def test_a_stack_of_mixers_and_attention_layers(gdn):
+    """verify (a programmatic dependent) -> append -> attention, layer upon layer on one stream, over shared scratch, as a
+    hybrid stack runs them: the results of the same calls one by one, eagerly and from a graph."""
+    from gated_deltanet_mixer_verify_b200.inputs import make_inputs, workload
+    from gdn_helpers import to_dev
+    w = workload("single_seq_verify")
+    L0 = make_inputs(w, layer=0)["accept_len"].numpy()
+    mix = [to_dev(make_inputs(w, layer=i, accept_len=L0, gates="gentle")) for i in range(4)]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)  # noqa: E731
+    B, T, Hq, Hk, d, page, past = 1, mix[0]["q"].shape[1], 24, 4, 256, 64, 9000
+    pages = -(-(past + T) // page) + 400
+    layers = [dict(q=r(B, T, Hq, d), k=r(B, T, Hk, d), v=r(B, T, Hk, d), kc=r(pages, page, Hk, d), vc=r(pages, page, Hk, d)) for _ in mix]
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(1, -1)
+    kv, ql = _i32([past + T]), _i32([T])
+    pos = torch.arange(past, past + T, device="cuda")
+    slots = (table[0, pos // page].long() * page + pos % page).view(B, T)
+    freq = torch.tensor(1e6 ** (-np.arange(0, 64, 2) / 64), dtype=F32, device="cuda")
+    q_out, ws = torch.empty(B, T, Hq, d, dtype=BF, device="cuda"), torch.empty(gdn.paged_attention_workspace_bytes(B, T, Hq, Hk, d), dtype=torch.uint8,
+                                                                               device="cuda")
+
+    def run(states, caches, outs, one_by_one=False):
+        for m, a, st, (kc, vc), (om, oa) in zip(mix, layers, states, caches, outs):
+            gdn.verify_step(m["q"], m["k"], m["v"], m["a"], m["b"], m["A_log"], m["dt_bias"], st, st, m["accept_len"], om, pdl=not one_by_one)
+            if one_by_one:
+                torch.cuda.synchronize()
+            gdn.rope_append(a["q"], a["k"], a["v"], freq, kc, vc, slots, kv_len=kv, q_len=ql, q_out=q_out)
+            if one_by_one:
+                torch.cuda.synchronize()
+            gdn.paged_attention(q_out, kc, vc, table, kv, q_len=ql, o=oa, workspace=ws)
+            if one_by_one:
+                torch.cuda.synchronize()
+
+    def fresh():
+        return ([m["S0"].clone() for m in mix], [(a["kc"].clone(), a["vc"].clone()) for a in layers],
+                [(torch.zeros(m["v"].shape, device="cuda"), torch.zeros(B, T, Hq, d, dtype=BF, device="cuda")) for m in mix])
+
+    want = fresh()
+    run(*want, one_by_one=True)
+    flat = lambda x: [*x[0], *(t for p in x[1] + x[2] for t in p)]  # noqa: E731
+    for _ in range(3):
+        got = fresh()
+        torch.cuda.synchronize()
+        run(*got)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
+    got = fresh()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(*got)
+    for a, b in zip(flat(got), flat(fresh())):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
+
 
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_verify_loop(gdn, dt):
