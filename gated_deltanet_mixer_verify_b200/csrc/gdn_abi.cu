@@ -669,6 +669,13 @@ static gdn_status check_heads(const gdn_kv_shape* s, const char* who) {
     return GDN_OK;
 }
 
+// Whether n bytes at x and m bytes at y overlap.
+static bool meet(const void* x, size_t n, const void* y, size_t m) {
+    const char* a = static_cast<const char*>(x);
+    const char* b = static_cast<const char*>(y);
+    return a < b + m && b < a + n;
+}
+
 static int64_t element_bytes(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
 // The cache's strides: 16-byte multiples, no two entries of an axis within one head's d elements.
@@ -733,11 +740,6 @@ gdn_status gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* seq_len_in, int
             {free_list, (size_t)shape->num_pages * 4, -1}};
         const struct { const void* p; size_t n; } in[] = {
             {seq_len_in, nb}, {n_pages_in, nb}, {free_count_in, 4}, {commit_len, nb}, {add_len, nb}, {block_len, nb}};
-        const auto meet = [](const void* x, size_t n, const void* y, size_t m) {
-            const char* a = static_cast<const char*>(x);
-            const char* b = static_cast<const char*>(y);
-            return a < b + m && b < a + n;
-        };
         for (int i = 0; i < 8; ++i) {
             for (int j = 0; j < 6; ++j)
                 if (in[j].p && !(out[i].in == j && out[i].p == in[j].p) && meet(out[i].p, out[i].n, in[j].p, in[j].n))
@@ -912,16 +914,22 @@ static gdn_status paged_attention(const gdn_kv_shape* shape, float scale, int32_
     REQUIRE_PTR(o, who);
     if (lse) REQUIRE_PTR(lse, who);
     const size_t rows = (size_t)shape->B * shape->T * shape->H_q;
-    const char* qp = static_cast<const char*>(q);
-    const char* op = static_cast<const char*>(o);
-    if (qp < op + rows * shape->d * element_bytes(shape->out_dtype) && op < qp + rows * shape->d * element_bytes(shape->dtype))
-        return fail(GDN_ERR_INVALID_ARG, "%s: o overlaps q", who);
     const size_t need = gdn::paged_attention_workspace_bytes(shape->B, shape->T, shape->H_q, shape->H_kv, shape->d,
                                                              shape->dtype == GDN_BF16);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
     if (workspace && !aligned16(workspace))
         return fail(GDN_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", who);
+    // What the call writes may be nothing else that it reads or writes.
+    const size_t counts = (size_t)shape->B * 4;
+    const struct { const char* name; const void* p; size_t n; } mem[] = {
+        {"o", o, rows * shape->d * element_bytes(shape->out_dtype)}, {"lse", lse, rows * 4}, {"the workspace", workspace, need},
+        {"q", q, rows * shape->d * element_bytes(shape->dtype)}, {"block_table", block_table, counts * shape->max_pages},
+        {"kv_len", kv_len, counts}, {"q_len", q_len, counts}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (mem[i].p && mem[j].p && meet(mem[i].p, mem[i].n, mem[j].p, mem[j].n))
+                return fail(GDN_ERR_INVALID_ARG, "%s: %s overlaps %s", who, mem[i].name, mem[j].name);
     gdn::AttnArgs a = {};
     a.B = shape->B;
     a.T = shape->T;

@@ -523,6 +523,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  *   0..max_pages * page_size or q_len[b] outside 0..T writes nothing (GDN_STATUS_BAD_LENGTH).
  *   Positions on a page id outside the pool are not seen (GDN_STATUS_BAD_PAGE).
  *   GDN_STATUS_WAIT_TIMEOUT: a CTA gave up; the rows of the sequences and key heads it was at were not written.
+ *   o, lse and the workspace must not overlap one another, nor anything that the call reads.
  *   workspace  gdn_paged_attention_workspace_bytes, 16-byte aligned, contents irrelevant on entry;
  *              calls that may overlap on the GPU need one each (two captured graphs included).
  * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products

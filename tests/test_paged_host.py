@@ -126,6 +126,20 @@ def test_attention_refusals(gdn):
     assert call(_shape(gdn, B=0), q=None) == 0
 
 
+def test_attention_refuses_what_it_writes_over_what_it_uses(gdn):
+    names = ["q", "k", "v", "table", "kv_len", "q_len", "o", "lse", "ws"]
+    at = {n: FAKE * 8 * (i + 1) for i, n in enumerate(names)}
+    need = gdn.paged_attention_workspace_bytes(2, 8, 24, 4, 128)
+    size = dict(q=2 * 8 * 24 * 128 * 2, o=2 * 8 * 24 * 128 * 2, lse=2 * 8 * 24 * 4, ws=need, table=2 * 8 * 4, kv_len=8, q_len=8)
+    call = lambda **kw: gdn.lib().gdn_paged_attention(_shape(gdn), 0.1, 0, *dict(at, **kw).values(), need, None)  # noqa: E731
+    for out in ("o", "lse", "ws"):
+        for other in size:
+            if other == out:
+                continue
+            for p in (at[other], at[other] + (size[other] - 1) // 16 * 16, at[other] - (size[out] - 1) // 16 * 16):
+                assert call(**{out: p}) == INVALID and "overlaps" in _err(gdn), (out, other)
+
+
 def test_attention_selftest_refusals(gdn):
     at = [FAKE * (i + 1) for i in range(9)]
     call = lambda polls, *p: gdn.lib().gdn_selftest_attention_wait(_shape(gdn), 0.1, 0, *(p or at), 1 << 40, polls, None)  # noqa: E731
