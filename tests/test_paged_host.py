@@ -128,7 +128,7 @@ def test_attention_refusals(gdn):
 
 def test_attention_refuses_what_it_writes_over_what_it_uses(gdn):
     names = ["q", "k", "v", "table", "kv_len", "q_len", "o", "lse", "ws"]
-    at = {n: FAKE * 8 * (i + 1) for i, n in enumerate(names)}
+    at = {n: FAKE * 64 * (i + 1) for i, n in enumerate(names)}
     need = gdn.paged_attention_workspace_bytes(2, 8, 24, 4, 128)
     size = dict(q=2 * 8 * 24 * 128 * 2, o=2 * 8 * 24 * 128 * 2, lse=2 * 8 * 24 * 4, ws=need, table=2 * 8 * 4, kv_len=8, q_len=8)
     call = lambda **kw: gdn.lib().gdn_paged_attention(_shape(gdn), 0.1, 0, *dict(at, **kw).values(), need, None)  # noqa: E731
