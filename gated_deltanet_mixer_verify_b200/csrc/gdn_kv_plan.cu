@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_kv_plan_kernel(const __grid_c
                         const unsigned pos = (unsigned)s_len[j] + t, pg = pos / page;
                         const int id = (int)pg < s_held[j] ? a.table[(size_t)(b0 + j) * a.max_pages + pg]
                                                            : a.free_list[have - 1 - s_k0[j] - ((int)pg - s_held[j])];
-                        slot[k] = (int64_t)id * page + (pos - pg * page);
+                        if ((unsigned)id < (unsigned)a.num_pages) slot[k] = (int64_t)id * page + (pos - pg * page);
+                        else status |= kStatusBadPage;
                     }
                 }
 #pragma unroll
@@ -238,7 +239,9 @@ __global__ void __launch_bounds__(256) gdn_kv_slots_kernel(const __grid_constant
         int64_t slot = -1;
         if (t < q) {
             const unsigned pos = (unsigned)(a.kv_len[b] - q + t), pg = pos / page;
-            slot = (int64_t)a.table[(size_t)b * a.max_pages + pg] * page + (pos - pg * page);
+            const int id = a.table[(size_t)b * a.max_pages + pg];
+            if ((unsigned)id < (unsigned)a.num_pages) slot = (int64_t)id * page + (pos - pg * page);
+            else if (a.status_word) atomicOr(a.status_word, kStatusBadPage);
         }
         a.slots[i] = slot;
     }

@@ -459,7 +459,8 @@ typedef struct {
  * keeps them with kv_len = q_len = 0 (both GDN_STATUS_BAD_LENGTH). Growth is granted in order of b
  * until the first sequence that does not fit into what is free: it and every later one that needs
  * pages get none, and neither does one that would need more than max_pages; their q_len is 0 and
- * their kv_len is len (GDN_STATUS_NO_PAGES).
+ * their kv_len is len (GDN_STATUS_NO_PAGES). A new token whose page id, from block_table or free_list, is outside the pool
+ * has the slot -1 (GDN_STATUS_BAD_PAGE).
  */
 gdn_status gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* seq_len_in, int32_t* seq_len_out,
                        const int32_t* commit_len, const int32_t* block_len, const int32_t* add_len,

@@ -136,6 +136,31 @@ def test_plan_free_count_that_cannot_be(gdn):
         assert int(st) == 4 and int(c) == want
 
 
+@pytest.mark.parametrize("T", [5, 9000])
+@pytest.mark.parametrize("bad", [-1, -3, 40, (1 << 31) - 1, -(1 << 31)])
+def test_plan_pages_that_cannot_be(gdn, bad, T):
+    # ids outside the pool, in a page that is held and among the free: their tokens have no slot (a negative id would
+    # make a negative slot, which means none, without a word), all others theirs
+    page, pages = 16, 40
+    width = -(-(T + 20) // page) + 1
+    table = np.full((2, width), -1, np.int32)
+    table[0, 0], table[1, 0] = bad, 7
+    free = np.arange(8, 40, dtype=np.int32)
+    free[31] = bad                                   # the first to be handed out
+    for slots_in in (4, 12):
+        st = _status()
+        add = min(T, 20)
+        tb, fr = _i32(table), _i32(np.concatenate([free, np.zeros(8, np.int32)]))
+        kv, ql, slots = gdn.kv_plan(_i32([slots_in, slots_in]), _i32([1, 1]), tb, fr, _i32([32]), T, page, add_len=_i32([add, add]), status_word=st)
+        tb, slots = tb.cpu().numpy(), slots.cpu().numpy()
+        assert int(st) == 8 and kv.tolist() == [slots_in + add] * 2 and ql.tolist() == [add] * 2
+        for b in range(2):
+            for t in range(T):
+                pos = slots_in + t
+                ok = t < add and 0 <= tb[b, pos // page] < pages
+                assert slots[b, t] == (int(tb[b, pos // page]) * page + pos % page if ok else -1), (b, t)
+
+
 def test_plan_empty_batch_and_zero_adds(gdn):
     e = lambda *sh, dt=torch.int32: torch.empty(sh, dtype=dt, device="cuda")  # noqa: E731
     count = _i32([5])
