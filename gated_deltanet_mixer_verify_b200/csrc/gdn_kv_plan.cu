@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_kv_plan_kernel(const __grid_c
         carry += total;
     }
     const int64_t have = carry < a.num_pages ? carry : a.num_pages;
+    if (carry > a.num_pages) status |= kStatusBadLength;   // some page was free, or somebody else's, already
     __syncthreads();
 
     // Pages handed out from the top, in the same order, while they last; then the slots.

@@ -460,7 +460,8 @@ typedef struct {
  * until the first sequence that does not fit into what is free: it and every later one that needs
  * pages get none, and neither does one that would need more than max_pages; their q_len is 0 and
  * their kv_len is len (GDN_STATUS_NO_PAGES). A new token whose page id, from block_table or free_list, is outside the pool
- * has the slot -1 (GDN_STATUS_BAD_PAGE).
+ * has the slot -1 (GDN_STATUS_BAD_PAGE). A free_count_in outside 0..num_pages counts as the nearer of the two, and returned
+ * pages that the full list has no room for are dropped (both GDN_STATUS_BAD_LENGTH).
  */
 gdn_status gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* seq_len_in, int32_t* seq_len_out,
                        const int32_t* commit_len, const int32_t* block_len, const int32_t* add_len,

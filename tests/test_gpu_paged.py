@@ -161,6 +161,19 @@ def test_plan_pages_that_cannot_be(gdn, bad, T):
                 assert slots[b, t] == (int(tb[b, pos // page]) * page + pos % page if ok else -1), (b, t)
 
 
+@pytest.mark.parametrize("B", [2, 1500])
+def test_plan_more_pages_back_than_there_are(gdn, B):
+    # pages returned onto a list that is full already: they are dropped, and it is said
+    count, st = _i32([6]), _status()
+    free = _i32([3, 1, 4, 0, 5, 2, -9])
+    held = np.zeros(B, np.int32)
+    held[-1] = 2
+    table = np.full((B, 4), -1, np.int32)
+    table[-1, :2] = 6, 3
+    gdn.kv_plan(_i32([0] * B), _i32(held), _i32(table), free, count, 2, 16, add_len=_i32([-1] * B), status_word=st)
+    assert int(st) == 4 and int(count) == 7 and free.tolist() == [3, 1, 4, 0, 5, 2, 6]
+
+
 def test_plan_empty_batch_and_zero_adds(gdn):
     e = lambda *sh, dt=torch.int32: torch.empty(sh, dtype=dt, device="cuda")  # noqa: E731
     count = _i32([5])
