@@ -790,7 +790,7 @@ bool tc_applies(const AttnArgs& a) {
     if (!a.bf16 || a.cache.page % 8 != 0 || a.cache.page_stride > most || a.cache.slot_stride > most || a.cache.head_stride > most)
         return false;
     const int rows = a.Hq / a.Hk * a.T;
-    const int64_t elements = (int64_t)a.B * a.Hk * a.max_pages * a.cache.page * a.d;   // of K that the tables can hold
+    const double elements = (double)a.B * a.Hk * a.max_pages * a.cache.page * a.d;     // of K that the tables can hold
     if (a.d == 64) return rows > 32 && elements >= 1 << 21;
     if (a.d == 128) return rows > 16 && elements >= 1 << 21;
     return elements >= (rows > 16 ? 1 << 22 : 1 << 23);
