@@ -11,12 +11,12 @@
 // A warp's maxima, totals and sums are joined with the other warps' when the CTA leaves the item.
 //
 // Bound: HBM. Measured, bf16, one row per sequence: 64 sequences of 500 .. 16,384 positions, 32 heads over 8, d 128
-// (2.2 GB) 352 us, 96% of the measured copy rate; 128 sequences of 1 .. 2048, 16 heads over 16 (1.07 GB) 193 us,
-// 85% (2,048 short items: their beginnings and ends); one sequence of 1,024 12 us, latency: the page numbers, the
-// values and the join one after another. fp32 (three products for one, 16 sequences, window 1000) 20 us, latency too.
-// One wave of CTAs, because more cost: two, three, four waves 354, 361, 367 and 197, 203, 209 us. An item counts
-// as three units more: with 2, 3, 5, 7 the second case took 208, 193, 188, 193 us, all others the same within 2%
-// but 32 sequences of 100 .. 2048 (d 128) 27.0, 26.1, 26.7, 28.1.
+// (2.2 GB) 356 to 403 us a call by the machine, 84 to 95% of the measured copy rate; 128 sequences of 1 .. 2048, 16 heads
+// over 16 (1.07 GB) 204 to 218 us, 75 to 80% (2,048 short items: their beginnings and ends); one sequence of 1,024 12.7 us, latency: the page
+// numbers, the values and the join one after another. fp32 (three products for one, 16 sequences, window 1000) 21 us, latency too.
+// One wave of CTAs, because more cost: one, two, three, four waves 352, 354, 361, 367 and 193, 197, 203, 209 us (in a graph, before
+// the last steps on precision). An item counts as three units more: with 2, 3, 5, 7 the second case took 208, 193, 188, 193 us then,
+// all others the same within 2% but 32 sequences of 100 .. 2048 (d 128) 27.0, 26.1, 26.7, 28.1.
 //
 // Precision. bf16 products are exact in fp32. The weights 2^(s - m) enter the second product as two
 // bf16 terms (2^-17 relative), because one (2^-9) would be as large as the rounding of a bf16
@@ -26,7 +26,8 @@
 // they form short sums only, and ordinary additions, which round, put those together.
 // Measured, 64 sequences of 4096 positions, 16 heads over 4, values of one, mean error of the outputs (formed in the units:
 // all in them): d 64 -5.9e-8 (-1.4e-6), 136 us (133); d 128 -6.5e-8 (-1.8e-6), 371 us (342); d 256 -5.8e-8
-// (-2.5e-6), 956 us (821); summing each half of a stage apart -4e-8, 137, 393, 1064 us. bf16, 80 sequences of 16,384: d 64
+// (-2.5e-6), 956 us (821); summing each half of a stage apart -4e-8, 137, 393, 1064 us. (With the look at scores that are
+// NaN they take 139, 387 and 979.) bf16, 80 sequences of 16,384: d 64
 // -2.9e-8 (-2.4e-6), d 128 -3.3e-8 (-3.0e-6); the first and second case above take 2 and 4% longer for it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -29,13 +29,13 @@
 // bound by their reads of A from shared memory). In the steady state a tile takes 4,900 cycles where all
 // SMs hold the same number of them; beside it stand the first tiles (the pages' numbers, keys, scores and values
 // one after another: 20 us cold) and the ends of items (the maxima anew, the look, the output: 2 tiles).
-// Measured: one sequence of 32K positions, 8 rows x 6 heads, d 256 (134 MB) 46 us; 32 of 100 .. 8192 (546 MB)
-// 113 to 118 us, 4.7 TB/s, 72% of the measured copy rate.
+// Measured: one sequence of 32K positions, 8 rows x 6 heads, d 256 (134 MB) 43 us; 32 of 100 .. 8192 (546 MB)
+// 110 to 118 us a call, 4.6 to 5.0 TB/s, 71 to 76% of the measured copy rate.
 // Steps, the first of these cases, us: rows as M, one thread per row, P in tensor memory 71; positions as M with the
 // steps of a tile one after the other 68; overlapped, and the join's grid small 56; programmatic dependents 51 to 54;
-// the look in rows at once, the next queries before the last look, items weighted 3 46.
+// the look in rows at once, the next queries before the last look, items weighted 3 46; a loop without exits 43.
 // What lies behind a sequence in its last page costs the look at up to 15 positions and the call 9% if all of it is NaN (the
-// second case: 115.0 us, 125.0; d 128 81.2, 89.0; d 64 77.8, 85.0).
+// second case: 110.5 us, 120.2; d 128 77.6, 85.1; d 64 71.2, 78.2).
 // Not faster: fetching with cp.async (5,600 to 9,800 cycles a tile; the proxy fence waits for copies in flight).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,7 +54,8 @@ using namespace dev;
 
 constexpr int kTile = 128;                      // positions per tile, and per unit
 // Units that an item costs besides (its first and last steps overlap little). Measured with 2, 3, 4, us: one sequence of
-// 32K positions (d 256, 48 rows) 52.3, 45.8, 47.5; 32 sequences of 100 .. 8192 117.9, 113.5, 112.9; 128 of 100 .. 512 97.7, 96.5, 96.2.
+// 32K positions (d 256, 48 rows) 47.1, 42.6, 44.2; 32 sequences of 100 .. 8192 125, 110.9, 111.3 (d 128: 88, 76.5, 68.7; d 64: 81.5,
+// 71.8, 64.9).
 constexpr int kExtra = 3;
 constexpr int kBlock = kTile * 128;             // bytes of [128 positions][64 columns]
 constexpr float kGrow = 16.f;                   // a score this far (base 2) above its row's maximum moves the maxima
@@ -64,12 +65,12 @@ constexpr int kMaskRing = 16;                   // more tiles than the ring hold
 constexpr int kRows = 64;                       // rows of a row tile at most
 // Tiles whose products are added up in the matrix units. Those cut where they add, always towards zero, so a sum formed in them
 // all along loses with every tile (128 tiles, values of one: 2.0e-5 of it); sums of kFold tiles are therefore put together
-// by ordinary additions, which round, in tensor memory beside O: 2.2e-6, however long the sequence. It takes 3% of the second
-// case below (d 128: 2%, one sequence 1%; with folds of 8 tiles 4%, and no less with 32), and half the tensor memory at d 256, which is why a
-// tile has 64 rows: with 128 of them, 640 threads of 96 registers that spilled and two ring slots at d 256, calls of 96 and 128 rows took
-// us, 64 then 128 rows a tile: d 64 40 and 40, 47 and 50 (one sequence of 32K), 112 and 114, 112 and 124 (32 of 4096); d 128
-// 44 and 45, 49 and 53; 121 and 124, 118 and 133; d 256 63 and 66, 68 and 72; 165 and 171, 158 and 177.
-constexpr int kFold = 16;
+// by ordinary additions, which round, in tensor memory beside O: 1.2e-6, however long the sequence. Calls take as long with folds of
+// 8, 16 and 32 tiles as with none (the second case below 110.9, 110.9, 111.0, 110.8 us). It needs half the tensor memory at d 256, which
+// is why a tile has 64 rows: with 128 of them (640 threads of 96 registers that spilled, two ring slots at d 256) calls of 96 and
+// 128 rows took us, 64 then 128 rows a tile: d 64 40 and 40, 47 and 50 (one sequence of 32K), 112 and 114, 112 and 124 (32 of
+// 4096); d 128 44 and 45, 49 and 53; 121 and 124, 118 and 133; d 256 63 and 66, 68 and 72; 165 and 171, 158 and 177.
+constexpr int kFold = 8;
 
 // D columns of the head.
 template <int D>

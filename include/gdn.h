@@ -531,7 +531,7 @@ gdn_status gdn_rope_append(const gdn_kv_shape* shape, const gdn_rope* rope, cons
  * Sums and softmax statistics are fp32; with a bf16 cache the weights e^{s_j} enter the products
  * with v as two bf16 terms (2^-17 relative). fp32 products are formed from split tf32 terms
  * (about 2^-22; finite values of v from 2^127 (2 - 2^-11) on count as infinite). Sums over positions are
- * formed in the matrix units, which cut, in pieces only (2,048 positions of a bf16 cache at most: 2^-18 of a sum),
+ * formed in the matrix units, which cut, in pieces only (1,024 positions of a bf16 cache at most: 2^-19 of a sum),
  * put together by additions that round: no error grows with the length but theirs. The result does not depend
  * on the order in which CTAs finish.
  * shape: B 0..65535, T 1..16, d 64, 128 or 256, H_q <= 65535.

@@ -656,8 +656,8 @@ def test_attention_long_fp32_sums_do_not_drift(gdn, d):
 def test_attention_long_bf16_sums_do_not_drift(gdn, d, page, T):
     # As above, of a bf16 cache: 160 items of 65,536 positions (all over the same pages), so that a CTA holds whole ones, on the
     # tensor-memory kernel (page 16) and the streaming one. A product of 16 positions cuts its sum by less than
-    # 2^-23 of it; 2 of them go into each sum of the streaming kernel, 256 into each of the other's, whose first half
-    # of growth counts half: 2^-22 and 2^-16 at most, however long the sequence; the additions that put those
+    # 2^-23 of it; 2 of them go into each sum of the streaming kernel, 128 into each of the other's (256 are allowed for), whose
+    # first half of growth counts half: 2^-22 and 2^-16 at most, however long the sequence; the additions that put those
     # together round to either side (2^-24 each, 2^-22 in the mean is allowed). Sums formed in the units all along
     # lose 8e-5 and 1e-5 here.
     S, Hq, Hk = 65536, 12, 2
