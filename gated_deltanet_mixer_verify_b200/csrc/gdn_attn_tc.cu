@@ -192,6 +192,9 @@ __device__ __forceinline__ float reduce32(float* v, int lane) {
 // see it, and sums that such values turned into NaN are looked up again. The first stands at the positions before
 // lo_max and behind p_min, a block's length each at most; what all rows see stands between. to: where the rows
 // were stored (-1: nowhere); k: what they were scaled with (0 or NaN where the sums of their weights are).
+// Slow, as nothing but infinities that rows see leads to a long look: 32 sequences of 8,192 positions with infinities in all columns
+// take 4.2 ms (0.15 without), with NaN 0.4. What stands between looked up once for a column instead of once for 16 rows: 2.2 ms, but
+// 114 us for 110 in calls without (registers).
 __device__ __noinline__ void mend(const Args& x, int b, int h, int col, int first, int end, Sight see, int share, int row, int n, bool repair, bool whole,
                                   const int64_t* to, const float* k) {
     using E = __nv_bfloat16;
